@@ -1,4 +1,5 @@
-"""Build ``libw4a16.so`` (HIP kernels + C ABI) for gfx950 with hipcc, in-tree.
+"""Build ``libw4a16.so`` and ``libmxfp4.so`` (HIP kernels + C ABI) for gfx950 with
+hipcc, in-tree.
 
     python -m weight_only_int4_gemv_amd.build
 """
@@ -17,6 +18,10 @@ LIBRARY = os.path.join(PKG, "libw4a16.so")
 SOURCES = ["api.hip", "quantize.hip", "gemv.hip", "gemv_chain.hip", "gemm_mfma.hip",
            "gemm_skinny.hip", "gemv_mfma4.hip", "gemm_batched.hip", "gemv_q4_0.hip",
            "gather_x.hip"]
+# The MXFP4 linear layer and its mixture-of-experts form (include/mxfp4.h).
+MXFP4_LIBRARY = os.path.join(PKG, "libmxfp4.so")
+MXFP4_SOURCES = ["mxfp4_api.hip", "mxfp4_quantize.hip", "mxfp4_stream.hip", "mxfp4_matmul.hip",
+                 "moe_route.hip"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",
@@ -42,13 +47,15 @@ def hipcc() -> str:
 
 
 def build(verbose: bool = False) -> str:
-    """Compile every source (in parallel) and link the shared library."""
+    """Compile every source (in parallel) and link the shared libraries; returns
+    the path of ``libw4a16.so``."""
     with tempfile.TemporaryDirectory(prefix="w4a16_build_") as tmp:
         procs = []
-        objects = []
-        for src in SOURCES:
-            obj = os.path.join(tmp, src.replace(".hip", ".o"))
-            objects.append(obj)
+        def obj_of(src):
+            return os.path.join(tmp, src.replace(".hip", ".o"))
+
+        for src in SOURCES + MXFP4_SOURCES:
+            obj = obj_of(src)
             cmd = [hipcc(), *HIPCC_FLAGS, "-c", os.path.join(CSRC, src), "-o", obj]
             if verbose:
                 print(" ".join(cmd), flush=True)
@@ -65,10 +72,12 @@ def build(verbose: bool = False) -> str:
                 print("\n".join(lines))
         if failed:
             raise RuntimeError("hipcc failed on " + ", ".join(failed))
-        tmp_lib = LIBRARY + ".tmp%d" % os.getpid()
-        cmd = [hipcc(), "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp_lib, *objects]
-        subprocess.run(cmd, check=True, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
-        os.replace(tmp_lib, LIBRARY)
+        for library, sources in ((LIBRARY, SOURCES), (MXFP4_LIBRARY, MXFP4_SOURCES)):
+            tmp_lib = library + ".tmp%d" % os.getpid()
+            cmd = [hipcc(), "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp_lib,
+                   *map(obj_of, sources)]
+            subprocess.run(cmd, check=True, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+            os.replace(tmp_lib, library)
     return LIBRARY
 
 

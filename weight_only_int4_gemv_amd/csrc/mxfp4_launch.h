@@ -1,0 +1,53 @@
+// mxfp4_launch.h — host-side launchers of the MXFP4 and expert kernels
+// (private).  Shapes, alignment and sizes are validated by the C ABI
+// (mxfp4_api.hip) before any of these is called; no output is empty.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace mxfp4 {
+
+enum DType { kF16 = 0, kBF16 = 1, kF32 = 2 };
+
+hipError_t launch_quantize(const void* X, DType dt, int64_t rows, int64_t K, int64_t stride,
+                           uint8_t* codes, uint8_t* scales, hipStream_t stream);
+hipError_t launch_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t n, void* Y,
+                             DType dt, hipStream_t stream);
+
+// The weight-only product.  Dense: offsets NULL, E = 1, x_rows = R = M.
+struct LinearArgs {
+    const uint16_t* X;
+    const int* tokens;          // NULL: row r of X
+    const uint8_t* codes;
+    const uint8_t* scales;
+    const int* offsets;         // NULL: all R rows belong to expert 0
+    uint16_t* Y;
+    int64_t x_stride;
+    int x_rows, R, E;
+    int N;                      // weight rows per expert
+    int K;
+    int swiglu;                 // Y has N / 2 columns
+};
+// Grid of `slots` row tiles by nblocks column blocks: slot = z * gridDim.y + y
+// (slots past the last tile do nothing).
+inline dim3 slot_grid(int nblocks, int64_t slots) {
+    const int64_t y = slots < 32768 ? slots : 32768;
+    return dim3((unsigned)nblocks, (unsigned)y, (unsigned)((slots + y - 1) / y));
+}
+// Few rows per weight matrix: weights straight into matrix-core registers.
+hipError_t launch_stream(const LinearArgs& a, DType dt, hipStream_t stream);
+
+hipError_t launch_matmul(const uint8_t* a_codes, const uint8_t* a_scales, int64_t M,
+                         const uint8_t* b_codes, const uint8_t* b_scales, int64_t N, int64_t K,
+                         void* Y, DType dt, hipStream_t stream);
+
+hipError_t launch_route(const void* logits, DType dt, int T, int E, int64_t stride, int k,
+                        bool renormalize, int* ids, float* weights, hipStream_t stream);
+int64_t plan_blocks(int64_t R);          // blocks of choices; one needs no workspace
+hipError_t launch_plan(const int* ids, int R, int k, int E, int* offsets, int* tokens,
+                       int* positions, int* counts, hipStream_t stream);
+hipError_t launch_combine(const uint16_t* Y, DType dt, int R, int N, const int* positions,
+                          const float* weights, int T, int k, uint16_t* out, hipStream_t stream);
+
+}  // namespace mxfp4

@@ -1,0 +1,138 @@
+// mxfp4_quantize.hip — quantization to MXFP4 and back.
+//
+// Per block of 32 columns: E = floor(log2 max|x|) - 2, code = x / 2^E rounded
+// to the nearest e2m1 value (ties to even, saturated at 6).  The division by a
+// power of two is exact, so the rounding is one instruction per two elements
+// (the scaled fp4 conversions); what bounds both kernels is memory.
+#include "mxfp4_device.h"
+#include "mxfp4_launch.h"
+
+namespace mxfp4 {
+namespace {
+
+// Eight elements a lane: 16 bytes of a 16-bit type, 32 of fp32; four
+// neighbouring lanes share a block.
+template <DType DT>
+struct In {
+    float v[8];
+    uint32_t peak;      // fp32 bits of max |v|; all-ones exponent: not finite
+    __device__ __forceinline__ void load(const void* X, int64_t i) {
+        if constexpr (DT == kF32) {
+            const float4_t a = *(const float4_t*)((const float*)X + i);
+            const float4_t b = *(const float4_t*)((const float*)X + i + 4);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) { v[j] = a[j]; v[4 + j] = b[j]; }
+        } else {
+            const uint4_t a = *(const uint4_t*)((const uint16_t*)X + i);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if constexpr (DT == kBF16) {
+                    v[2 * j] = __builtin_bit_cast(float, a[j] << 16);
+                    v[2 * j + 1] = __builtin_bit_cast(float, a[j] & 0xFFFF0000u);
+                } else {
+                    v[2 * j] = F16::load((uint16_t)a[j]);
+                    v[2 * j + 1] = F16::load((uint16_t)(a[j] >> 16));
+                }
+            }
+        }
+        peak = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            peak = max(peak, __builtin_bit_cast(uint32_t, v[j]) & 0x7FFFFFFFu);
+    }
+};
+
+// A grid dimension holds fewer than 2^32 threads: larger matrices loop.
+constexpr int64_t kMaxBlocks = (int64_t)1 << 23;
+
+// Row r = blockIdx.y + n gridDim.y, lane chunk = 8 columns.  A dense matrix is
+// passed as one row.  K % 32 == 0, so the four lanes of a block stay together.
+template <DType DT>
+__global__ __launch_bounds__(256) void quantize_kernel(const void* X, int64_t rows, int64_t K,
+                                                       int64_t stride, uint8_t* codes,
+                                                       uint8_t* scales) {
+    for (int64_t r = blockIdx.y; r < rows; r += gridDim.y) {
+        for (int64_t chunk = (int64_t)blockIdx.x * 256 + threadIdx.x; chunk < K / 8;
+             chunk += (int64_t)gridDim.x * 256) {
+            In<DT> in;
+            in.load(X, r * stride + chunk * 8);
+            const uint32_t peak = quad_max(in.peak);
+            const uint32_t field = peak >> 23;          // exponent + 127
+            uint32_t byte = field > 2 ? field - 2 : 0;
+            if (peak == 0) byte = 127;
+            const bool bad = field == 255;
+            const float s = scale_value(byte);
+            uint32_t w = 0;
+            w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, in.v[0], in.v[1], s, 0);
+            w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, in.v[2], in.v[3], s, 1);
+            w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, in.v[4], in.v[5], s, 2);
+            w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, in.v[6], in.v[7], s, 3);
+            const int64_t at = r * (K / 8) + chunk;
+            ((uint32_t*)codes)[at] = bad ? 0u : w;
+            if ((threadIdx.x & 3) == 0) scales[at >> 2] = bad ? 255 : (uint8_t)byte;
+        }
+    }
+}
+
+template <DType DT>
+__global__ __launch_bounds__(256) void dequantize_kernel(const uint32_t* codes,
+                                                         const uint8_t* scales, int64_t words,
+                                                         void* Y) {
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < words;
+         i += (int64_t)gridDim.x * 256) {
+    const uint32_t w = codes[i];
+    const float s = scale_value(scales[i >> 2]);
+    if constexpr (DT == kF32) {
+        const float2_t a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, s, 0);
+        const float2_t b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, s, 1);
+        const float2_t c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, s, 2);
+        const float2_t d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, s, 3);
+        ((float4_t*)Y)[2 * i] = (float4_t){a[0], a[1], b[0], b[1]};
+        ((float4_t*)Y)[2 * i + 1] = (float4_t){c[0], c[1], d[0], d[1]};
+    } else if constexpr (DT == kBF16) {
+        ((bf168_t*)Y)[i] = values8(w, s, BF16());
+    } else {
+        ((half8_t*)Y)[i] = values8(w, s, F16());
+    }
+    }
+}
+
+unsigned blocks_for(int64_t threads) {
+    const int64_t n = (threads + 255) / 256;
+    return (unsigned)(n < kMaxBlocks ? n : kMaxBlocks);
+}
+
+}  // namespace
+
+hipError_t launch_quantize(const void* X, DType dt, int64_t rows, int64_t K, int64_t stride,
+                           uint8_t* codes, uint8_t* scales, hipStream_t stream) {
+    if (stride == K) {                    // dense: one long row
+        K *= rows;
+        stride = K;
+        rows = 1;
+    }
+    const dim3 grid(blocks_for(K / 8), (unsigned)(rows < 65535 ? rows : 65535));
+    if (dt == kF16)
+        quantize_kernel<kF16><<<grid, 256, 0, stream>>>(X, rows, K, stride, codes, scales);
+    else if (dt == kBF16)
+        quantize_kernel<kBF16><<<grid, 256, 0, stream>>>(X, rows, K, stride, codes, scales);
+    else
+        quantize_kernel<kF32><<<grid, 256, 0, stream>>>(X, rows, K, stride, codes, scales);
+    return hipGetLastError();
+}
+
+hipError_t launch_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t n, void* Y,
+                             DType dt, hipStream_t stream) {
+    const int64_t words = n / 8;
+    const unsigned grid = blocks_for(words);
+    const uint32_t* c = (const uint32_t*)codes;
+    if (dt == kF16)
+        dequantize_kernel<kF16><<<grid, 256, 0, stream>>>(c, scales, words, Y);
+    else if (dt == kBF16)
+        dequantize_kernel<kBF16><<<grid, 256, 0, stream>>>(c, scales, words, Y);
+    else
+        dequantize_kernel<kF32><<<grid, 256, 0, stream>>>(c, scales, words, Y);
+    return hipGetLastError();
+}
+
+}  // namespace mxfp4
