@@ -161,8 +161,8 @@ int mxfp4_linear(const void* X, int dtype, int64_t M, int64_t x_stride, const ui
 }
 
 size_t mxfp4_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-    (void)M, (void)N, (void)K;
-    return 0;
+    if (bad_size(M) || bad_size(N) || check_k(K)) return 0;
+    return mxfp4::matmul_workspace(M, N, K);
 }
 
 int mxfp4_matmul(const uint8_t* a_codes, const uint8_t* a_scales, int64_t M,
@@ -184,7 +184,7 @@ int mxfp4_matmul(const uint8_t* a_codes, const uint8_t* a_scales, int64_t M,
     if (outputs_overlap(out, in)) return W4A16_ERR_INVALID_ARG;
     if (const int st = check_device()) return st;
     return status_of(mxfp4::launch_matmul(a_codes, a_scales, M, b_codes, b_scales, N, K, Y,
-                                          dtype_of(dtype), stream_of(stream)));
+                                          dtype_of(dtype), (float*)workspace, stream_of(stream)));
 }
 
 int moe_route(const void* logits, int dtype, int64_t T, int64_t E, int64_t stride, int64_t k,

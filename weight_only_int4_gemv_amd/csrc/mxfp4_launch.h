@@ -35,12 +35,17 @@ inline dim3 slot_grid(int nblocks, int64_t slots) {
     const int64_t y = slots < 32768 ? slots : 32768;
     return dim3((unsigned)nblocks, (unsigned)y, (unsigned)((slots + y - 1) / y));
 }
+constexpr int64_t kMaxGrid = (int64_t)1 << 22;      // blocks of a launch (threads stay below 2^32)
+
 // Few rows per weight matrix: weights straight into matrix-core registers.
 hipError_t launch_stream(const LinearArgs& a, DType dt, hipStream_t stream);
 
+// Product of two MXFP4 matrices.  part: matmul_workspace bytes for the partial
+// sums of K slices, or NULL for no split.
+size_t matmul_workspace(int64_t M, int64_t N, int64_t K);
 hipError_t launch_matmul(const uint8_t* a_codes, const uint8_t* a_scales, int64_t M,
                          const uint8_t* b_codes, const uint8_t* b_scales, int64_t N, int64_t K,
-                         void* Y, DType dt, hipStream_t stream);
+                         void* Y, DType dt, float* part, hipStream_t stream);
 
 hipError_t launch_route(const void* logits, DType dt, int T, int E, int64_t stride, int k,
                         bool renormalize, int* ids, float* weights, hipStream_t stream);
