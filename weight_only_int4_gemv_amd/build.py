@@ -20,8 +20,8 @@ SOURCES = ["api.hip", "quantize.hip", "gemv.hip", "gemv_chain.hip", "gemm_mfma.h
            "gather_x.hip"]
 # The MXFP4 linear layer and its mixture-of-experts form (include/mxfp4.h).
 MXFP4_LIBRARY = os.path.join(PKG, "libmxfp4.so")
-MXFP4_SOURCES = ["mxfp4_api.hip", "mxfp4_quantize.hip", "mxfp4_stream.hip", "mxfp4_matmul.hip",
-                 "moe_route.hip"]
+MXFP4_SOURCES = ["mxfp4_api.hip", "mxfp4_quantize.hip", "mxfp4_stream.hip", "mxfp4_tiled.hip",
+                 "mxfp4_matmul.hip", "moe_route.hip"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",

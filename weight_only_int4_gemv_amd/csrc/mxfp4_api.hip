@@ -125,8 +125,8 @@ int mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, 
 }
 
 size_t mxfp4_linear_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-    (void)M, (void)N, (void)K;
-    return 0;
+    if (bad_size(M) || bad_size(N) || check_k(K)) return 0;
+    return mxfp4::linear_workspace(M, N, K);
 }
 
 int mxfp4_linear(const void* X, int dtype, int64_t M, int64_t x_stride, const uint8_t* codes,
@@ -157,7 +157,8 @@ int mxfp4_linear(const void* X, int dtype, int64_t M, int64_t x_stride, const ui
     a.E = 1;
     a.N = (int)N;
     a.K = (int)K;
-    return status_of(mxfp4::launch_stream(a, dtype_of(dtype), stream_of(stream)));
+    return status_of(mxfp4::launch_linear(a, dtype_of(dtype), (float*)workspace,
+                                          stream_of(stream)));
 }
 
 size_t mxfp4_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K) {
@@ -273,7 +274,7 @@ int mxfp4_grouped_linear(const void* X, int dtype, int64_t x_rows, int64_t x_str
     a.N = (int)N;
     a.K = (int)K;
     a.swiglu = swiglu != 0;
-    return status_of(mxfp4::launch_stream(a, dtype_of(dtype), stream_of(stream)));
+    return status_of(mxfp4::launch_linear(a, dtype_of(dtype), nullptr, stream_of(stream)));
 }
 
 int moe_combine(const void* Y, int dtype, int64_t R, int64_t N, const int32_t* positions,

@@ -28,6 +28,11 @@ struct LinearArgs {
     int N;                      // weight rows per expert
     int K;
     int swiglu;                 // Y has N / 2 columns
+    // Set by launch_linear.
+    float* part;                // fp32 partial sums [slices][R][N], or NULL
+    int slices, steps;          // K slices, steps of a slice
+    int mt, nt;                 // row tiles (dense), column blocks
+    int64_t first;              // first block of this launch
 };
 // Grid of `slots` row tiles by nblocks column blocks: slot = z * gridDim.y + y
 // (slots past the last tile do nothing).
@@ -37,8 +42,16 @@ inline dim3 slot_grid(int nblocks, int64_t slots) {
 }
 constexpr int64_t kMaxGrid = (int64_t)1 << 22;      // blocks of a launch (threads stay below 2^32)
 
+// The weight-only product by the kernel that suits its sizes.  part:
+// linear_workspace bytes for the partial sums of K slices, or NULL for no split.
+size_t linear_workspace(int64_t M, int64_t N, int64_t K);
+hipError_t launch_linear(LinearArgs a, DType dt, float* part, hipStream_t stream);
 // Few rows per weight matrix: weights straight into matrix-core registers.
 hipError_t launch_stream(const LinearArgs& a, DType dt, hipStream_t stream);
+
+// Y = the K slices' partial sums [slices][n], added in slice order.
+void launch_add_slices(const float* part, int slices, int64_t n, void* Y, DType dt,
+                       hipStream_t stream);
 
 // Product of two MXFP4 matrices.  part: matmul_workspace bytes for the partial
 // sums of K slices, or NULL for no split.

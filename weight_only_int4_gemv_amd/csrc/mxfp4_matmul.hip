@@ -328,16 +328,13 @@ __global__ __launch_bounds__(256) void add_slices_kernel(const float* part, int 
 }
 
 template <DType DT>
-void add_slices(const MatmulArgs& a, hipStream_t stream) {
+void add_slices(const float* part, int slices, int64_t n, void* Y, hipStream_t stream) {
     typedef typename Out<DT>::type out_t;
-    const int64_t n = (int64_t)a.M * a.N;
-    const bool wide = n % 4 == 0 && (uintptr_t)a.Y % (4 * sizeof(out_t)) == 0;
+    const bool wide = n % 4 == 0 && (uintptr_t)Y % (4 * sizeof(out_t)) == 0;
     const int64_t threads = wide ? n / 4 : n, blocks = (threads + 255) / 256;
     const unsigned grid = (unsigned)(blocks < (1 << 20) ? blocks : 1 << 20);
-    if (wide)
-        add_slices_kernel<DT, 4><<<grid, 256, 0, stream>>>(a.part, a.slices, n, (out_t*)a.Y);
-    else
-        add_slices_kernel<DT, 1><<<grid, 256, 0, stream>>>(a.part, a.slices, n, (out_t*)a.Y);
+    if (wide) add_slices_kernel<DT, 4><<<grid, 256, 0, stream>>>(part, slices, n, (out_t*)Y);
+    else add_slices_kernel<DT, 1><<<grid, 256, 0, stream>>>(part, slices, n, (out_t*)Y);
 }
 
 typedef Tiling<256, 256, 128, 64, 8, 2> Large;     // one block a CU
@@ -396,6 +393,13 @@ void launch(MatmulArgs a, DType dt, hipStream_t stream) {
 
 }  // namespace
 
+void launch_add_slices(const float* part, int slices, int64_t n, void* Y, DType dt,
+                       hipStream_t stream) {
+    if (dt == kF16) add_slices<kF16>(part, slices, n, Y, stream);
+    else if (dt == kBF16) add_slices<kBF16>(part, slices, n, Y, stream);
+    else add_slices<kF32>(part, slices, n, Y, stream);
+}
+
 size_t matmul_workspace(int64_t M, int64_t N, int64_t K) {
     if (M <= 0 || N <= 0) return 0;
     const Choice c = choose(M, N, K, true);
@@ -414,11 +418,7 @@ hipError_t launch_matmul(const uint8_t* a_codes, const uint8_t* a_scales, int64_
     if (c.tiling == 0) launch<Large>(a, dt, stream);
     else if (c.tiling == 1) launch<Medium>(a, dt, stream);
     else launch<Small>(a, dt, stream);
-    if (a.part) {
-        if (dt == kF16) add_slices<kF16>(a, stream);
-        else if (dt == kBF16) add_slices<kBF16>(a, stream);
-        else add_slices<kF32>(a, stream);
-    }
+    if (a.part) launch_add_slices(a.part, a.slices, (int64_t)a.M * a.N, Y, dt, stream);
     return hipGetLastError();
 }
 

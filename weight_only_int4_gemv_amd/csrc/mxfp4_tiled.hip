@@ -1,0 +1,441 @@
+// mxfp4_tiled.hip — weight-only MXFP4 product for many rows (prefill, larger
+// batches, experts with tens of rows and more): 16-bit X times MXFP4 weights,
+// dequantized in registers, on the 32x32x16 matrix instructions.
+//
+// A block owns BM rows of X and BN weight rows; each of its waves all BM rows
+// and WN weight rows, so that a weight is converted once per block.  K is
+// walked in steps of 64 columns: X and code tiles go from global memory
+// straight to LDS, kStages tiles deep, scales 16 blocks of a row at a time
+// through registers.  The sum over k may run in any order as long as both
+// operands agree: half h of a wave takes block h of the step (16 bytes of
+// codes and one scale a lane), MFMA i its columns 8i .. 8i+7.
+//
+// With SwiGLU a block's weight rows are 32 gate rows, their 32 up rows, the
+// next 32 gate rows ..., so that a wave holds both factors of its outputs.
+#include "mxfp4_launch.h"
+#include "mxfp4_tile.h"
+
+namespace mxfp4 {
+namespace {
+
+constexpr int kStepCols = 64;
+constexpr int kXRow = kStepCols * 2;        // bytes of a row of the X tile
+constexpr int kGroup = 32;                  // weight rows copied together
+constexpr int kGroupBytes = kGroup * kStepCols / 2;
+constexpr int kScaleBlocks = 16;            // blocks of a row whose scales are staged together
+constexpr int kScaleSteps = kScaleBlocks * kBlock / kStepCols;
+
+// What rows of zeros are read from (no token, columns past K).
+__device__ const uint4_t kZeros = {0, 0, 0, 0};
+
+template <int BM_, int WN_, int WAVES, int STAGES>
+struct Tiling {
+    static constexpr int BM = BM_, WN = WN_, BN = WN * WAVES;
+    static constexpr int MT = BM / 32, NT = WN / 32;
+    static constexpr int kWaves = WAVES, kThreads = WAVES * kWave, kStages = STAGES;
+    static constexpr int kXBytes = BM * kXRow, kStage = kXBytes + BN / kGroup * kGroupBytes;
+    static constexpr int kScales = BN * kScaleBlocks;
+    static constexpr int kXRows = 8 * WAVES;                // rows of one X copy of every wave
+    static constexpr int kXCopies = BM / kXRows;
+    static constexpr int kWCopies = BN / kGroup / WAVES;
+    static constexpr int kCopies = kXCopies + kWCopies;     // per wave and step
+    static constexpr int kScaleRows = (BN + kThreads - 1) / kThreads;
+    static constexpr int kPitch = WN + 4;
+    static constexpr int kTurn = 32 * kPitch * 4;           // a wave's 32 rows in fp32
+    static constexpr int kLoop = STAGES * kStage + 2 * kScales;
+    static constexpr int kLds = kLoop > kTurn * WAVES ? kLoop : kTurn * WAVES;
+    static_assert(BM % kXRows == 0 && kXRows % 16 == 0, "a lane's copies share their swizzle");
+    static_assert(BN % (kGroup * WAVES) == 0, "whole groups a wave");
+};
+
+// 16-byte chunk c of row r of the X tile stands at c ^ x_swizzle(r), block b of
+// weight row r of a group at b ^ w_swizzle(r): 16 lanes that read the same chunk
+// of 16 rows meet all 64 banks once.
+__device__ __forceinline__ int x_swizzle(int r) { return (r >> 1) & 7; }
+__device__ __forceinline__ int w_swizzle(int r) { return (r >> 3) & 1; }
+
+template <typename T, class C>
+__global__ __launch_bounds__(C::kThreads, 2) void tiled_kernel(LinearArgs a) {
+    constexpr bool kIsF16 = __is_same(T, F16);
+    constexpr int MT = C::MT, NT = C::NT;
+    typedef typename T::vec8 vec8;
+    __shared__ __align__(1024) char lds[C::kLds];
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int F = a.swiglu ? a.N / 2 : a.N;                 // columns of Y
+    const int per = a.swiglu ? C::BN / 2 : C::BN;           // of one block
+
+    // Tile of this block.  Grouped: column blocks innermost, so that blocks of one
+    // row tile run together.  Dense: bands of kBand row tiles, row tiles innermost.
+    constexpr int kBand = 8;
+    const int64_t id = a.first + xcd_order(blockIdx.x, gridDim.x);
+    Tile t;
+    int nb, slice = 0;
+    if (a.offsets != nullptr) {
+        const int64_t slot = id / a.nt;
+        nb = (int)(id - slot * a.nt);
+        t = find_tile(a.offsets, a.E, a.R, C::BM, (int)slot);
+        t.expert = __builtin_amdgcn_readfirstlane(t.expert);
+        t.row0 = __builtin_amdgcn_readfirstlane(t.row0);
+        t.rows = __builtin_amdgcn_readfirstlane(t.rows);
+    } else {
+        const int64_t tiles = (int64_t)a.mt * a.nt, run = (int64_t)kBand * a.nt;
+        slice = (int)(id / tiles);
+        const int64_t tile = id - slice * tiles;
+        const int band = (int)(tile / run), in_band = (int)(tile - band * run);
+        const int high = min(kBand, a.mt - band * kBand);
+        t.expert = 0;
+        t.row0 = (band * kBand + in_band % high) * C::BM;
+        t.rows = min(C::BM, a.R - t.row0);
+        nb = in_band / high;
+    }
+    if (t.rows <= 0) return;
+    const int col0 = nb * per;
+    const int KB = a.K / kBlock, row_bytes = a.K / 2;
+    const int step0 = slice * a.steps;
+    const int steps = t.expert < 0 ? 0 : min(a.steps, (KB + 1) / 2 - step0);
+    // K % 64 == 32: the last step's second block lies past K.
+    const int odd_step = (KB & 1) ? KB / 2 - step0 : -1;
+    const uint32_t base = lds_address(lds);
+
+    // First weight row (of the expert) of group g, and how many of its 32 exist.
+    auto group_row = [&](int g) {
+        return a.swiglu ? (g & 1) * F + col0 + (g >> 1) * kGroup : col0 + g * kGroup;
+    };
+    auto group_rows = [&](int g) {
+        return min(kGroup, F - (a.swiglu ? col0 + (g >> 1) * kGroup : col0 + g * kGroup));
+    };
+    const int64_t expert_row = (int64_t)max(t.expert, 0) * a.N;
+
+    // Copies.  X: wave w, copy c: the 8 rows from (c * kWaves + w) * 8 on.
+    const int x_row = wave * 8 + lane / 8, x_chunk = (lane & 7) ^ x_swizzle(x_row);
+    const char* xp[C::kXCopies];
+    uint32_t live = 0;
+#pragma unroll
+    for (int c = 0; c < C::kXCopies; ++c) {
+        const int r = t.row0 + min(x_row + c * C::kXRows, t.rows - 1);   // not stored past rows
+        const int src = a.tokens ? a.tokens[r] : r;
+        const bool ok = src >= 0 && src < a.x_rows;
+        xp[c] = ok ? (const char*)(a.X + src * a.x_stride + step0 * kStepCols + x_chunk * 8)
+                   : (const char*)&kZeros;
+        live |= (ok ? kXRow : 0u) << c;
+    }
+    uint4_t wrsrc[C::kWCopies];
+#pragma unroll
+    for (int j = 0; j < C::kWCopies; ++j) {
+        const int g = j * C::kWaves + wave, rows = group_rows(g);
+        wrsrc[j] = make_rsrc(a.codes + (expert_row + (rows > 0 ? group_row(g) : 0)) * row_bytes,
+                             (uint32_t)max(rows, 0) * row_bytes);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) wrsrc[j][i] = __builtin_amdgcn_readfirstlane(wrsrc[j][i]);
+    }
+    uint32_t w_off = (uint32_t)(lane / 2) * row_bytes + step0 * (kStepCols / 2) +
+                     ((lane & 1) ^ w_swizzle(lane / 2)) * 16;
+    auto copy = [&](int s) {
+        const uint32_t to = base + s % C::kStages * C::kStage;
+#pragma unroll
+        for (int c = 0; c < C::kXCopies; ++c) {
+            const char* p = s == odd_step && x_chunk >= 4 ? (const char*)&kZeros : xp[c];
+            copy16(p, to + (c * C::kXRows + wave * 8) * kXRow);
+            xp[c] += (live >> c) & kXRow;
+        }
+        // Blocks past K are the next row's first codes (or 0): they meet zeros.
+#pragma unroll
+        for (int j = 0; j < C::kWCopies; ++j)
+            copy16(wrsrc[j], w_off, 0, to + C::kXBytes + (j * C::kWaves + wave) * kGroupBytes);
+        w_off += kStepCols / 2;
+    };
+
+    // Scales: thread t takes rows t, t + kThreads, ...; LDS holds word w (blocks
+    // 4w ..) of row r at [w][r].  Blocks past K count as 1.
+    const uint8_t* srow[C::kScaleRows];
+    uint4_t sreg[C::kScaleRows];
+#pragma unroll
+    for (int i = 0; i < C::kScaleRows; ++i) {
+        const int r = min((int)threadIdx.x + i * C::kThreads, C::BN - 1), g = r / kGroup;
+        const int rows = group_rows(g);
+        srow[i] = a.scales + (expert_row + (rows > 0 ? group_row(g) + min(r % kGroup, rows - 1) : 0)) * KB;
+    }
+    auto load_scale_chunk = [&](int c) {
+        const int kb = step0 * 2 + c * kScaleBlocks;
+#pragma unroll
+        for (int i = 0; i < C::kScaleRows; ++i)
+            if (kb + kScaleBlocks <= KB) __builtin_memcpy(&sreg[i], srow[i] + kb, 16);   // any byte
+    };
+    auto store_scale_chunk = [&](int c) {
+        const int kb = step0 * 2 + c * kScaleBlocks;
+        char* at = lds + C::kStages * C::kStage + (c & 1) * C::kScales;
+#pragma unroll
+        for (int i = 0; i < C::kScaleRows; ++i) {
+            const int r = threadIdx.x + i * C::kThreads;
+            if (C::BN % C::kThreads != 0 && r >= C::BN) break;
+            if (kb + kScaleBlocks <= KB) {
+#pragma unroll
+                for (int w = 0; w < 4; ++w) ((uint32_t*)at)[w * C::BN + r] = sreg[i][w];
+            } else {
+#pragma unroll 1
+                for (int b = 0; b < kScaleBlocks; ++b)
+                    at[(b / 4 * C::BN + r) * 4 + b % 4] = kb + b < KB ? srow[i][kb + b] : 127;
+            }
+        }
+    };
+
+    // Fragments of the wave.
+    const int half = lane >> 5, r31 = lane & 31;
+    const int x_at = r31 * kXRow;
+    int x_off[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x_off[i] = x_at + ((4 * half + i) ^ x_swizzle(r31)) * 16;
+    const int w_at = C::kXBytes + wave * NT * kGroupBytes + r31 * 16 * 2 + (half ^ w_swizzle(r31)) * 16;
+    auto load_x = [&](vec8 (&x)[MT], const char* stage, int i) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m) x[m] = *(const vec8*)(stage + x_off[i] + m * 32 * kXRow);
+    };
+    auto load_w = [&](uint4_t (&w)[NT], float (&sc)[NT], bool& wide, int s) {
+        const char* stage = lds + s % C::kStages * C::kStage;
+        const int in = s % kScaleSteps;
+        const uint32_t* words = (const uint32_t*)(lds + C::kStages * C::kStage +
+                                                  (s / kScaleSteps & 1) * C::kScales);
+        bool out = false;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            w[n] = *(const uint4_t*)(stage + w_at + n * kGroupBytes);
+            const uint32_t b = words[in / 2 * C::BN + wave * C::WN + 32 * n + r31] >>
+                               (16 * (in & 1) + 8 * half) & 255;
+            out |= !f16_scale_ok(b);
+            sc[n] = scale_value(b);
+        }
+        wide = kIsF16 && __any(out);
+    };
+    float16_t acc[MT][NT] = {};
+    auto multiply = [&](const vec8 (&x)[MT], const vec8 (&w)[NT]) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) acc[m][n] = T::mfma32(w[n], x[m], acc[m][n]);
+    };
+
+    if (steps > 0) {
+        load_scale_chunk(0);
+#pragma unroll
+        for (int s = 0; s < C::kStages; ++s)
+            if (s < steps) copy(s);
+        store_scale_chunk(0);
+        wait_copies<0>();
+
+        vec8 x[2][MT], wv[2][NT];
+        uint4_t codes[NT];
+        float sc[NT];
+        bool wide;
+        // To step s + 1: every wave has read the last of step s, so its tile is
+        // free for the copy kStages on.
+        auto advance = [&](int s) {
+            if (s + 1 >= steps) return;
+            if ((s + 1) % kScaleSteps == 0) store_scale_chunk((s + 1) / kScaleSteps);
+            if (s + C::kStages <= steps) wait_copies<(C::kStages - 2) * C::kCopies>();
+            else wait_copies<0>();
+            if (s + C::kStages < steps) copy(s + C::kStages);
+            load_w(codes, sc, wide, s + 1);
+        };
+        load_w(codes, sc, wide, 0);
+        load_x(x[0], lds, 0);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) wv[0][n] = values8(codes[n][0], sc[n], T());
+        int s = 0;
+        // A step's first fragments are read while the matrix cores work on the
+        // last ones of the step before.
+        for (; s < steps; ++s) {
+            if (kIsF16 && wide) break;
+            const char* stage = lds + s % C::kStages * C::kStage;
+            if (s % kScaleSteps == 0 && s + kScaleSteps < steps)
+                load_scale_chunk(s / kScaleSteps + 1);
+#pragma unroll
+            for (int i = 0; i < 3; ++i) {
+                load_x(x[(i + 1) & 1], stage, i + 1);
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    wv[(i + 1) & 1][n] = values8(codes[n][i + 1], sc[n], T());
+                multiply(x[i & 1], wv[i & 1]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            advance(s);
+            load_x(x[0], lds + (s + 1) % C::kStages * C::kStage, 0);
+            multiply(x[1], wv[1]);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) wv[0][n] = values8(codes[n][0], sc[n], T());
+        }
+        // From the first step with weights outside fp16's range on: weights are
+        // exact in bf16, X is the sum of two bf16 values.
+        for (; kIsF16 && s < steps; ++s) {
+            const char* stage = lds + s % C::kStages * C::kStage;
+            if (s % kScaleSteps == 0 && s + kScaleSteps < steps)
+                load_scale_chunk(s / kScaleSteps + 1);
+#pragma unroll 1
+            for (int i = 0; i < 4; ++i) {
+                bf168_t w[NT];
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    w[n] = values8(*(const uint32_t*)(stage + w_at + n * kGroupBytes + 4 * i),
+                                   sc[n], BF16());
+                const int off = x_at + ((4 * half + i) ^ x_swizzle(r31)) * 16;
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    bf168_t hi, lo;
+                    split_bf16(*(const half8_t*)(stage + off + m * 32 * kXRow), hi, lo);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        acc[m][n] = BF16::mfma32(w[n], hi, acc[m][n]);
+                        acc[m][n] = BF16::mfma32(w[n], lo, acc[m][n]);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            }
+            advance(s);
+        }
+        wait_copies<0>();
+    }
+
+    // Results: lane l holds row l % 32 of X and the weight rows 8 g + 4 half + i
+    // in registers 4 g + i.  Each wave turns 32 rows at a time in its own LDS, so
+    // that stores run along the rows of Y.
+    float* turn = (float*)(lds + wave * C::kTurn);
+    const int wcols = a.swiglu ? C::WN / 2 : C::WN;
+    const int wcol0 = col0 + wave * wcols, cols = min(wcols, F - wcol0);
+    const bool wide_out = F % 8 == 0 && (uintptr_t)a.Y % 16 == 0;
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            if (NT > 1 && a.swiglu && (n & 1)) continue;
+            const int at = r31 * C::kPitch + (a.swiglu ? n / 2 : n) * 32 + 4 * half;
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                float4_t v;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    v[i] = acc[m][n][4 * g + i];
+                    if (NT > 1 && a.swiglu) v[i] = silu(v[i]) * acc[m][n | 1][4 * g + i];
+                }
+                *(float4_t*)&turn[at + 8 * g] = v;
+            }
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        const int rows = min(32, t.rows - 32 * m);
+        const int64_t out0 = (int64_t)(t.row0 + 32 * m) * F + wcol0;
+        if (a.part != nullptr) {
+            float* p = a.part + (int64_t)slice * a.R * F + out0;
+            if (F % 4 == 0) {
+                for (int i = lane; i < 32 * C::WN / 4; i += kWave) {
+                    const int r = i / (C::WN / 4), c = i % (C::WN / 4) * 4;
+                    if (r < rows && c < cols)
+                        *(float4_t*)(p + (int64_t)r * F + c) = *(const float4_t*)&turn[r * C::kPitch + c];
+                }
+            } else {
+                for (int i = lane; i < 32 * C::WN; i += kWave) {
+                    const int r = i / C::WN, c = i % C::WN;
+                    if (r < rows && c < cols) p[(int64_t)r * F + c] = turn[r * C::kPitch + c];
+                }
+            }
+        } else if (wide_out) {
+            const int shift = a.swiglu ? 1 : 0;             // 8 columns a lane
+            for (int i = lane; i < 32 * C::WN / 8 >> shift; i += kWave) {
+                const int r = i / (C::WN / 8 >> shift), c = i % (C::WN / 8 >> shift) * 8;
+                uint16_t v[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = T::store(turn[r * C::kPitch + c + j]);
+                if (r < rows && c < cols)
+                    __builtin_memcpy(__builtin_assume_aligned(a.Y + out0 + (int64_t)r * F + c, 16), v, 16);
+            }
+        } else {
+            for (int i = lane; i < 32 * wcols; i += kWave) {
+                const int r = i / wcols, c = i % wcols;
+                if (r < rows && c < cols)
+                    a.Y[out0 + (int64_t)r * F + c] = T::store(turn[r * C::kPitch + c]);
+            }
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+    }
+}
+
+typedef Tiling<128, 64, 4, 3> Large;        // 128 x 256, two blocks a CU
+typedef Tiling<64, 64, 4, 4> Medium;        // 64 x 256, two
+typedef Tiling<64, 32, 4, 4> Small;         // 64 x 128, three
+
+template <class C>
+void launch(LinearArgs a, DType dt, hipStream_t stream) {
+    const int F = a.swiglu ? a.N / 2 : a.N, per = a.swiglu ? C::BN / 2 : C::BN;
+    a.nt = (F + per - 1) / per;
+    a.mt = (a.R + C::BM - 1) / C::BM;
+    const int64_t slots = a.offsets ? tile_slots(a.R, a.E, C::BM) : a.mt;
+    const int64_t blocks = slots * a.nt * a.slices;
+    for (a.first = 0; a.first < blocks; a.first += kMaxGrid) {
+        const unsigned grid = (unsigned)(blocks - a.first < kMaxGrid ? blocks - a.first : kMaxGrid);
+        if (dt == kF16)
+            tiled_kernel<F16, C><<<grid, C::kThreads, 0, stream>>>(a);
+        else
+            tiled_kernel<BF16, C><<<grid, C::kThreads, 0, stream>>>(a);
+    }
+}
+
+// Tiling and K split.
+//   Rows per expert on average (all rows of a dense product): few go to the
+//   stream kernel; many to Large, which reads each operand from LDS half as often.
+//   64 experts of 3584 x 4096, us by rows per expert (stream / Medium / Large):
+//   8: 190 / 182 / 214, 16: 285 / 178 / 261, 75: 816 / 278 / 322, 150: 1508 / 412
+//   / 446, 512: 4785 / 1115 / 1030.
+//   K slices (dense): where the tiles are fewer than what fits on 256 CUs, as
+//   many as fill them, of at least eight steps: 50 x 4096 x 14336 105 us
+//   unsplit, 24 in 8 or 16 slices; 200 rows 105 and 43 us.
+struct Choice {
+    int tiling;         // 0 stream, 1 large, 2 medium, 3 small
+    int slices, steps;
+};
+Choice choose(int64_t rows, int64_t R, int64_t N, int64_t K, bool grouped, bool split) {
+    const int64_t total = (K / kBlock + 1) / 2;
+    Choice c{0, 1, (int)total};
+    if (grouped) {
+        c.tiling = rows < 8 ? 0 : rows <= 192 ? 2 : 1;
+        return c;
+    }
+    if (rows <= 16) return c;
+    auto tiles = [&](int bm, int bn) { return (R + bm - 1) / bm * ((N + bn - 1) / bn); };
+    int64_t n = tiles(128, 256);
+    c.tiling = 1;
+    if (n < 256) n = tiles(64, 256), c.tiling = 2;
+    if (n < 256) n = tiles(64, 128), c.tiling = 3;
+    if (split) {
+        int64_t s = 512 / n;
+        if (s > 8) s = 8;
+        if (s > total / 8) s = total / 8;
+        if (s > 1) {
+            c.steps = (int)((total + s - 1) / s);
+            c.slices = (int)((total + c.steps - 1) / c.steps);
+        }
+    }
+    return c;
+}
+
+}  // namespace
+
+size_t linear_workspace(int64_t M, int64_t N, int64_t K) {
+    if (M <= 0 || N <= 0) return 0;
+    const Choice c = choose(M, M, N, K, false, true);
+    return c.slices > 1 ? (size_t)c.slices * M * N * sizeof(float) : 0;
+}
+
+hipError_t launch_linear(LinearArgs a, DType dt, float* part, hipStream_t stream) {
+    const bool grouped = a.offsets != nullptr;
+    const Choice c = choose(grouped ? a.R / a.E : a.R, a.R, a.N, a.K, grouped, part != nullptr);
+    a.slices = c.slices, a.steps = c.steps;
+    a.part = c.slices > 1 ? part : nullptr;
+    if (c.tiling == 0) return launch_stream(a, dt, stream);
+    if (c.tiling == 1) launch<Large>(a, dt, stream);
+    else if (c.tiling == 2) launch<Medium>(a, dt, stream);
+    else launch<Small>(a, dt, stream);
+    if (a.part) launch_add_slices(a.part, a.slices, (int64_t)a.R * a.N, a.Y, dt, stream);
+    return hipGetLastError();
+}
+
+}  // namespace mxfp4
