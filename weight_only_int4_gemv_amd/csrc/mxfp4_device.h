@@ -124,39 +124,59 @@ struct Tile {
     int rows;        // rows in it (1 .. bm); 0: no tile in this slot
 };
 
-// Tile of a slot, found by every wave for itself: lane l holds group l of
-// each 64 groups, a scan over the wave counts tiles.  Offsets are clamped to
+// Tiles of 64 groups, lane l holding group base + l.  Offsets are clamped to
 // [0, R], so that no value in them can lead out of bounds.
+struct Groups {
+    int lo, hi;      // rows of this lane's group
+    int first;       // tiles of the earlier lanes' groups
+    int count;       // tiles of all 64
+};
+__device__ __forceinline__ Groups scan_groups(const int* offsets, int E, int R, int bm, int base) {
+    const int lane = threadIdx.x & (kWave - 1), g = base + lane;
+    Groups w;
+    w.lo = w.hi = R;
+    if (g <= E + 1) {
+        w.lo = g == 0 ? 0 : min(max(offsets[g - 1], 0), R);
+        w.hi = g == E + 1 ? R : min(max(offsets[g], w.lo), R);
+    }
+    const int tiles = (w.hi - w.lo + bm - 1) / bm;
+    int sum = tiles;
+#pragma unroll
+    for (int d = 1; d < kWave; d <<= 1) {
+        const int up = __shfl_up(sum, d);
+        if (lane >= d) sum += up;
+    }
+    w.first = sum - tiles;
+    w.count = __builtin_amdgcn_readlane(sum, kWave - 1);
+    return w;
+}
+
+// Tiles in use, found by every wave for itself.
+__device__ __forceinline__ int count_tiles(const int* offsets, int E, int R, int bm) {
+    int n = 0;
+    for (int base = 0; base <= E + 1; base += kWave) n += scan_groups(offsets, E, R, bm, base).count;
+    return n;
+}
+
+// Tile of a slot.
 __device__ __forceinline__ Tile find_tile(const int* offsets, int E, int R, int bm, int slot) {
-    const int lane = threadIdx.x & (kWave - 1);
     int before = 0;
     for (int base = 0; base <= E + 1; base += kWave) {
-        const int g = base + lane;
-        int lo = R, hi = R;
-        if (g <= E + 1) {
-            lo = g == 0 ? 0 : min(max(offsets[g - 1], 0), R);
-            hi = g == E + 1 ? R : min(max(offsets[g], lo), R);
-        }
-        const int tiles = (hi - lo + bm - 1) / bm;
-        int sum = tiles;
-#pragma unroll
-        for (int d = 1; d < kWave; d <<= 1) {
-            const int up = __shfl_up(sum, d);
-            if (lane >= d) sum += up;
-        }
-        const int first = before + sum - tiles;      // tiles ahead of this group
+        const Groups w = scan_groups(offsets, E, R, bm, base);
+        const int first = before + w.first;
+        const int tiles = (w.hi - w.lo + bm - 1) / bm;
         const uint64_t hit = __ballot(slot >= first && slot < first + tiles);
         if (hit != 0) {
             const int src = __builtin_ctzll(hit);
             Tile t;
             t.expert = base + src - 1 < E ? base + src - 1 : -1;
-            const int r0 = __builtin_amdgcn_readlane(lo, src);
-            const int r1 = __builtin_amdgcn_readlane(hi, src);
+            const int r0 = __builtin_amdgcn_readlane(w.lo, src);
+            const int r1 = __builtin_amdgcn_readlane(w.hi, src);
             t.row0 = r0 + (slot - __builtin_amdgcn_readlane(first, src)) * bm;
             t.rows = min(bm, r1 - t.row0);
             return t;
         }
-        before += __builtin_amdgcn_readlane(sum, kWave - 1);
+        before += w.count;
     }
     return Tile{-1, 0, 0};
 }
