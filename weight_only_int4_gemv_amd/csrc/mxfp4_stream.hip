@@ -1,9 +1,9 @@
-// mxfp4_stream.hip — weight-only MXFP4 product for few rows per weight matrix
-// (decode, small batches, experts with a few rows each).
+// mxfp4_stream.hip — weight-only MXFP4 product for up to 16 rows per weight
+// matrix (decode, experts with a few rows each).
 //
 // What bounds it is reading the weights once: 17/32 byte per weight.  A block
-// owns 32 weight rows (two tiles of 16; with SwiGLU 16 gate rows and their 16
-// up rows) and 16 MT rows of X; its eight waves split K in chunks of 128
+// owns 16 J weight rows (J tiles; with SwiGLU J / 2 tiles of gate rows, then
+// their up rows) and 16 rows of X; its eight waves split K in chunks of 128
 // columns, each wave multiplies on the matrix cores, and the partial tiles are
 // added through LDS in wave order.
 //
@@ -12,6 +12,10 @@
 // k values of each.  The sum over k may run in any order as long as A and B
 // agree, so group g takes the whole block g of the chunk: one 16-byte load of
 // codes, one scale byte, and MFMA i multiplies its columns 8i .. 8i+7.
+//
+// A wave loads a chunk and multiplies it; other waves of the CU cover its wait
+// (holding a second chunk ahead costs as many waves as it gains: 1 x 4096 x
+// 14336 12.3 us against 12.7, 8 x 28672 x 8192 42.3 against 41.1).
 #include "mxfp4_device.h"
 #include "mxfp4_launch.h"
 
@@ -19,10 +23,10 @@ namespace mxfp4 {
 namespace {
 
 constexpr int kWaves = 8;
-constexpr int kChunk = 128;      // columns a wave takes at a time
+constexpr int kChunkBlocks = 4;  // blocks of a row a wave takes at a time
 constexpr int kTile = 16;
 
-template <typename T, int MT>
+template <typename T, int J>
 __global__ __launch_bounds__(kWaves* kWave) void stream_kernel(LinearArgs a) {
     constexpr bool kIsF16 = __is_same(T, F16);
     const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
@@ -30,145 +34,142 @@ __global__ __launch_bounds__(kWaves* kWave) void stream_kernel(LinearArgs a) {
 
     Tile t;
     if (a.offsets != nullptr) {
-        t = find_tile(a.offsets, a.E, a.R, kTile * MT, slot);
+        t = find_tile(a.offsets, a.E, a.R, kTile, slot);
     } else {
         t.expert = 0;
-        t.row0 = slot * kTile * MT;
-        t.rows = min(kTile * MT, a.R - t.row0);
+        t.row0 = slot * kTile;
+        t.rows = min(kTile, a.R - t.row0);
     }
     if (t.rows <= 0) return;
 
-    // Weight rows of the two tiles; rows past the end read the last row and
-    // are not stored.
+    // Weight rows of the tiles; rows past the end read the last row and are not
+    // stored.
     const int F = a.swiglu ? a.N / 2 : a.N;                 // columns of Y
-    const int col0 = nb * (a.swiglu ? kTile : 2 * kTile);   // first of this block
+    const int per = a.swiglu ? J * kTile / 2 : J * kTile;   // of this block
+    const int col0 = nb * per;
     const int KB = a.K / kBlock;
-    float4_t acc[2][MT] = {};
+    float4_t acc[J] = {};
 
     if (t.expert >= 0) {
-        const uint8_t* codes = a.codes + (int64_t)t.expert * a.N * (a.K / 2);
-        const uint8_t* scales = a.scales + (int64_t)t.expert * a.N * KB;
-        const uint8_t *wc[2], *ws[2];
+        const int64_t expert_row = (int64_t)t.expert * a.N;
+        const uint8_t *wc[J], *ws[J];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int64_t n = a.swiglu ? (int64_t)j * F + min(col0 + (lane & 15), F - 1)
-                                       : min(col0 + kTile * j + (lane & 15), F - 1);
-            wc[j] = codes + n * (a.K / 2);
-            ws[j] = scales + n * KB;
+        for (int j = 0; j < J; ++j) {
+            // SwiGLU: the gate tiles, then their up tiles.
+            const bool up = a.swiglu && j >= J / 2;
+            const int col = min(col0 + kTile * (up ? j - J / 2 : j) + (lane & 15), F - 1);
+            const int64_t n = expert_row + col + (up ? F : 0);
+            wc[j] = a.codes + n * (a.K / 2);
+            ws[j] = a.scales + n * KB;
         }
-        const uint16_t* xr[MT];
-        bool live[MT];
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            const int i = kTile * m + (lane & 15);
-            int src = -1;
-            if (i < t.rows) src = a.tokens ? a.tokens[t.row0 + i] : t.row0 + i;
-            live[m] = src >= 0 && src < a.x_rows;
-            xr[m] = a.X + (live[m] ? src : 0) * a.x_stride;
+        int src = -1;
+        if ((lane & 15) < t.rows) {
+            const int r = t.row0 + (lane & 15);
+            src = a.tokens ? a.tokens[r] : r;
         }
-        for (int c = wave * kChunk; c < a.K; c += kWaves * kChunk) {
-            const int kb = c / kBlock + (lane >> 4);
+        const bool live = src >= 0 && src < a.x_rows;
+        const uint16_t* xr = a.X + (live ? src : 0) * a.x_stride;
+
+        uint4_t w[J], x[4];
+        uint32_t sb[J];
+        auto load = [&](int c) {
+            const int kb = c * kChunkBlocks + (lane >> 4);
             const bool in = kb < KB;
-            uint4_t w[2] = {};
-            uint32_t sb[2] = {127, 127};
-            uint4_t x[MT][4] = {};
-            if (in) {
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
+            for (int j = 0; j < J; ++j) {
+                w[j] = (uint4_t){0, 0, 0, 0};
+                sb[j] = 127;
+                if (in) {
                     w[j] = *(const uint4_t*)(wc[j] + (int64_t)kb * 16);
                     sb[j] = ws[j][kb];
                 }
             }
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                if (in && live[m]) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        x[m][i] = *(const uint4_t*)(xr[m] + (int64_t)kb * kBlock + 8 * i);
-                }
+            for (int i = 0; i < 4; ++i) {
+                x[i] = (uint4_t){0, 0, 0, 0};
+                if (in && live) x[i] = *(const uint4_t*)(xr + (int64_t)kb * kBlock + 8 * i);
             }
-            float s[2];
+        };
+        auto multiply = [&]() {
+            float s[J];
+            bool ok = true;
 #pragma unroll
-            for (int j = 0; j < 2; ++j) s[j] = scale_value(sb[j]);
-            if (kIsF16 && __any(!(f16_scale_ok(sb[0]) && f16_scale_ok(sb[1])))) {
+            for (int j = 0; j < J; ++j) {
+                s[j] = scale_value(sb[j]);
+                ok = ok && f16_scale_ok(sb[j]);
+            }
+            if (kIsF16 && __any(!ok)) {
                 // Weights outside fp16's range: exact in bf16, X as two bf16.
 #pragma unroll
-                for (int m = 0; m < MT; ++m) {
+                for (int i = 0; i < 4; ++i) {
+                    bf168_t hi, lo;
+                    split_bf16(__builtin_bit_cast(half8_t, x[i]), hi, lo);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        bf168_t hi, lo;
-                        split_bf16(__builtin_bit_cast(half8_t, x[m][i]), hi, lo);
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            const bf168_t wv = values8(w[j][i], s[j], BF16());
-                            acc[j][m] = BF16::mfma16(wv, hi, acc[j][m]);
-                            acc[j][m] = BF16::mfma16(wv, lo, acc[j][m]);
-                        }
+                    for (int j = 0; j < J; ++j) {
+                        const bf168_t wv = values8(w[j][i], s[j], BF16());
+                        acc[j] = BF16::mfma16(wv, hi, acc[j]);
+                        acc[j] = BF16::mfma16(wv, lo, acc[j]);
                     }
                 }
             } else {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < 4; ++i)
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const typename T::vec8 wv = values8(w[j][i], s[j], T());
-#pragma unroll
-                        for (int m = 0; m < MT; ++m)
-                            acc[j][m] = T::mfma16(
-                                wv, __builtin_bit_cast(typename T::vec8, x[m][i]), acc[j][m]);
-                    }
-                }
+                    for (int j = 0; j < J; ++j)
+                        acc[j] = T::mfma16(values8(w[j][i], s[j], T()),
+                                           __builtin_bit_cast(typename T::vec8, x[i]), acc[j]);
             }
+        };
+        const int chunks = (KB + kChunkBlocks - 1) / kChunkBlocks;
+        load(wave);
+        for (int c = wave; c < chunks; c += kWaves) {
+            multiply();
+            if (c + kWaves < chunks) load(c + kWaves);
         }
     }
 
-    // Partial tiles through LDS: [wave][m tile][j][row of X][weight row].
-    __shared__ float part[kWaves][MT][2][kTile][kTile];
+    // Partial tiles through LDS: [wave][j][row of X][weight row].
+    __shared__ float part[kWaves][J][kTile][kTile];
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-            *(float4_t*)&part[wave][m][j][lane & 15][(lane >> 4) * 4] = acc[j][m];
+    for (int j = 0; j < J; ++j)
+        *(float4_t*)&part[wave][j][lane & 15][(lane >> 4) * 4] = acc[j];
     __syncthreads();
-    const int per_row = a.swiglu ? kTile : 2 * kTile;
-    for (int i = threadIdx.x; i < t.rows * per_row; i += kWaves * kWave) {
-        const int r = i / per_row, n = i % per_row;
+    for (int i = threadIdx.x; i < t.rows * per; i += kWaves * kWave) {
+        const int r = i / per, n = i % per;
         if (col0 + n >= F) continue;
         float h[2] = {0.0f, 0.0f};
-        const int j0 = a.swiglu ? 0 : n / kTile;
+        const int j0 = n / kTile;
 #pragma unroll
         for (int v = 0; v < kWaves; ++v) {
-            h[0] += part[v][r / kTile][j0][r % kTile][n % kTile];
-            if (a.swiglu) h[1] += part[v][r / kTile][1][r % kTile][n % kTile];
+            h[0] += part[v][j0][r][n % kTile];
+            if (J > 1 && a.swiglu) h[1] += part[v][j0 + J / 2][r][n % kTile];
         }
         const float y = a.swiglu ? silu(h[0]) * h[1] : h[0];
         a.Y[(int64_t)(t.row0 + r) * F + col0 + n] = T::store(y);
     }
 }
 
-template <typename T, int MT>
-hipError_t launch(const LinearArgs& a, hipStream_t stream) {
-    const int F = a.swiglu ? a.N / 2 : a.N;
-    const int per = a.swiglu ? kTile : 2 * kTile;
-    const int nblocks = (F + per - 1) / per;
-    const int64_t slots = a.offsets ? tile_slots(a.R, a.E, kTile * MT)
-                                    : (a.R + kTile * MT - 1) / (kTile * MT);
-    stream_kernel<T, MT><<<slot_grid(nblocks, slots), kWaves * kWave, 0, stream>>>(a);
+template <int J>
+hipError_t launch(const LinearArgs& a, DType dt, hipStream_t stream) {
+    const int F = a.swiglu ? a.N / 2 : a.N, per = a.swiglu ? J * kTile / 2 : J * kTile;
+    const int64_t slots = a.offsets ? tile_slots(a.R, a.E, kTile) : (a.R + kTile - 1) / kTile;
+    const dim3 grid = slot_grid((F + per - 1) / per, slots);
+    if (dt == kF16) stream_kernel<F16, J><<<grid, kWaves * kWave, 0, stream>>>(a);
+    else stream_kernel<BF16, J><<<grid, kWaves * kWave, 0, stream>>>(a);
     return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_stream(const LinearArgs& a, DType dt, hipStream_t stream) {
-    const int64_t rows = a.offsets ? a.R / a.E : a.R;      // per expert, on average
-    if (dt == kF16) {
-        if (rows <= 16) return launch<F16, 1>(a, stream);
-        if (rows <= 32) return launch<F16, 2>(a, stream);
-        return launch<F16, 4>(a, stream);
-    }
-    if (rows <= 16) return launch<BF16, 1>(a, stream);
-    if (rows <= 32) return launch<BF16, 2>(a, stream);
-    return launch<BF16, 4>(a, stream);
+    // Four tiles a block read X a quarter as often; one (with SwiGLU two) gives
+    // more blocks, and is faster where four leave CUs without one (us, one / two /
+    // four tiles): 8 x 28672 x 8192 59.9 / 48.6 / 41.1, 8 x 14336 x 4096 18.9 /
+    // 14.7 / 13.5, 8 x 4096 x 14336 17.3 / 23.0 / 38.3, 1 x 4096 x 4096 5.4 / 7.4
+    // / 11.8; four tokens, 8 of 64 experts, 4096 x 1792 39.5 / 37.0 / 31.0.
+    const int64_t slots = a.offsets ? tile_slots(a.R, a.E, kTile) : (a.R + kTile - 1) / kTile;
+    if (a.N / (4 * kTile) * slots >= 192) return launch<4>(a, dt, stream);
+    return a.swiglu ? launch<2>(a, dt, stream) : launch<1>(a, dt, stream);
 }
 
 }  // namespace mxfp4

@@ -37,7 +37,6 @@ __device__ __forceinline__ void copy16(const void* p, uint32_t lds) {
                  : "s"(lds), "v"(p)
                  : "memory");
 }
-
 // Waits until at most `left` of the wave's loads are in flight and its LDS
 // operations are done, then for the block's other waves.
 template <int LEFT>

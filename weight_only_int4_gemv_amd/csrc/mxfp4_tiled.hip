@@ -5,8 +5,8 @@
 // A block owns BM rows of X and BN weight rows; each of its waves all BM rows
 // and WN weight rows, so that a weight is converted once per block.  K is
 // walked in steps of 64 columns: X and code tiles go from global memory
-// straight to LDS, kStages tiles deep, scales 16 blocks of a row at a time
-// through registers.  The sum over k may run in any order as long as both
+// straight to LDS, kStages tiles deep, scales a chunk
+// of blocks of each row at a time through registers.  The sum over k may run in any order as long as both
 // operands agree: half h of a wave takes block h of the step (16 bytes of
 // codes and one scale a lane), MFMA i its columns 8i .. 8i+7.
 //
@@ -22,29 +22,31 @@ constexpr int kStepCols = 64;
 constexpr int kXRow = kStepCols * 2;        // bytes of a row of the X tile
 constexpr int kGroup = 32;                  // weight rows copied together
 constexpr int kGroupBytes = kGroup * kStepCols / 2;
-constexpr int kScaleBlocks = 16;            // blocks of a row whose scales are staged together
-constexpr int kScaleSteps = kScaleBlocks * kBlock / kStepCols;
 
 // What rows of zeros are read from (no token, columns past K).
 __device__ const uint4_t kZeros = {0, 0, 0, 0};
 
-template <int BM_, int WN_, int WAVES, int STAGES>
+template <int BM_, int WN_, int WAVES, int STAGES, int SCALE_BLOCKS, int PER_CU>
 struct Tiling {
+    static constexpr int kPerCu = PER_CU;                   // blocks on a CU
     static constexpr int BM = BM_, WN = WN_, BN = WN * WAVES;
     static constexpr int MT = BM / 32, NT = WN / 32;
     static constexpr int kWaves = WAVES, kThreads = WAVES * kWave, kStages = STAGES;
     static constexpr int kXBytes = BM * kXRow, kStage = kXBytes + BN / kGroup * kGroupBytes;
+    static constexpr int kScaleBlocks = SCALE_BLOCKS;       // scales of a row staged together
+    static constexpr int kScaleSteps = kScaleBlocks * kBlock / kStepCols;
     static constexpr int kScales = BN * kScaleBlocks;
     static constexpr int kXRows = 8 * WAVES;                // rows of one X copy of every wave
     static constexpr int kXCopies = BM / kXRows;
     static constexpr int kWCopies = BN / kGroup / WAVES;
     static constexpr int kCopies = kXCopies + kWCopies;     // per wave and step
-    static constexpr int kScaleRows = (BN + kThreads - 1) / kThreads;
     static constexpr int kPitch = WN + 4;
     static constexpr int kTurn = 32 * kPitch * 4;           // a wave's 32 rows in fp32
     static constexpr int kLoop = STAGES * kStage + 2 * kScales;
     static constexpr int kLds = kLoop > kTurn * WAVES ? kLoop : kTurn * WAVES;
     static_assert(BM % kXRows == 0 && kXRows % 16 == 0, "a lane's copies share their swizzle");
+    static_assert(kLds * PER_CU <= 160 * 1024, "blocks fit a CU");
+    static_assert(BN <= kThreads, "a row's scales a thread");
     static_assert(BN % (kGroup * WAVES) == 0, "whole groups a wave");
 };
 
@@ -55,7 +57,7 @@ __device__ __forceinline__ int x_swizzle(int r) { return (r >> 1) & 7; }
 __device__ __forceinline__ int w_swizzle(int r) { return (r >> 3) & 1; }
 
 template <typename T, class C>
-__global__ __launch_bounds__(C::kThreads, 2) void tiled_kernel(LinearArgs a) {
+__global__ __launch_bounds__(C::kThreads, C::kPerCu * C::kWaves / 4) void tiled_kernel(LinearArgs a) {
     constexpr bool kIsF16 = __is_same(T, F16);
     constexpr int MT = C::MT, NT = C::NT;
     typedef typename T::vec8 vec8;
@@ -67,7 +69,7 @@ __global__ __launch_bounds__(C::kThreads, 2) void tiled_kernel(LinearArgs a) {
 
     // Tile of this block.  Grouped: column blocks innermost, so that blocks of one
     // row tile run together; the XCDs share the tiles in use, not the slots (300
-    // tokens over 64 experts use 83 of 103 slots: 125 us by slots, BALANCED).  Dense: bands of kBand row tiles, row tiles innermost.
+    // tokens over 64 experts use 83 of 103 slots: 125 us by slots, 101 by tiles).  Dense: bands of kBand row tiles, row tiles innermost.
     constexpr int kBand = 8;
     int64_t blocks = gridDim.x;
     if (a.offsets != nullptr) {
@@ -153,38 +155,47 @@ __global__ __launch_bounds__(C::kThreads, 2) void tiled_kernel(LinearArgs a) {
         w_off += kStepCols / 2;
     };
 
-    // Scales: thread t takes rows t, t + kThreads, ...; LDS holds word w (blocks
-    // 4w ..) of row r at [w][r].  Blocks past K count as 1.
-    const uint8_t* srow[C::kScaleRows];
-    uint4_t sreg[C::kScaleRows];
+    // Scales: thread t holds kHeld blocks of row t in registers (half a cache line,
+    // so that lines are fetched once and the loop rarely waits for a load) and
+    // passes on kScaleBlocks at a time: LDS holds word w (blocks 4w ..) of row r
+    // at [w][r].  Blocks past K count as 1.
+    constexpr int kScaleBlocks = C::kScaleBlocks, kScaleSteps = C::kScaleSteps;
+    constexpr int kHeld = 64, kChunks = kHeld / kScaleBlocks;
+    const int s_row = min((int)threadIdx.x, C::BN - 1), s_rows = group_rows(s_row / kGroup);
+    const uint8_t* srow = a.scales + (expert_row + (s_rows > 0 ? group_row(s_row / kGroup) +
+                                      min(s_row % kGroup, s_rows - 1) : 0)) * KB + step0 * 2;
+    const int blocks_left = KB - step0 * 2;                 // from the slice's first on
+    uint32_t held[kHeld / 4];
+    auto load_scales = [&](int c) {                         // chunks c .. c + kChunks - 1
+        const int kb = c * kScaleBlocks;
 #pragma unroll
-    for (int i = 0; i < C::kScaleRows; ++i) {
-        const int r = min((int)threadIdx.x + i * C::kThreads, C::BN - 1), g = r / kGroup;
-        const int rows = group_rows(g);
-        srow[i] = a.scales + (expert_row + (rows > 0 ? group_row(g) + min(r % kGroup, rows - 1) : 0)) * KB;
-    }
-    auto load_scale_chunk = [&](int c) {
-        const int kb = step0 * 2 + c * kScaleBlocks;
-#pragma unroll
-        for (int i = 0; i < C::kScaleRows; ++i)
-            if (kb + kScaleBlocks <= KB) __builtin_memcpy(&sreg[i], srow[i] + kb, 16);   // any byte
+        for (int j = 0; j < kHeld / 8; ++j) {
+            uint2_t v = {0, 0};
+            if (kb + (j * 8 / kScaleBlocks + 1) * kScaleBlocks <= blocks_left)
+                __builtin_memcpy(&v, srow + kb + 8 * j, 8);     // any byte
+            held[2 * j] = v[0];
+            held[2 * j + 1] = v[1];
+        }
     };
     auto store_scale_chunk = [&](int c) {
-        const int kb = step0 * 2 + c * kScaleBlocks;
+        const int kb = c * kScaleBlocks;
         char* at = lds + C::kStages * C::kStage + (c & 1) * C::kScales;
+        if (C::BN < C::kThreads && threadIdx.x >= C::BN) return;
+        if (kb + kScaleBlocks <= blocks_left) {
 #pragma unroll
-        for (int i = 0; i < C::kScaleRows; ++i) {
-            const int r = threadIdx.x + i * C::kThreads;
-            if (C::BN % C::kThreads != 0 && r >= C::BN) break;
-            if (kb + kScaleBlocks <= KB) {
+            for (int w = 0; w < kScaleBlocks / 4; ++w) ((uint32_t*)at)[w * C::BN + s_row] = held[w];
 #pragma unroll
-                for (int w = 0; w < 4; ++w) ((uint32_t*)at)[w * C::BN + r] = sreg[i][w];
-            } else {
+            for (int w = 0; w < (kHeld - kScaleBlocks) / 4; ++w) held[w] = held[w + kScaleBlocks / 4];
+        } else {
 #pragma unroll 1
-                for (int b = 0; b < kScaleBlocks; ++b)
-                    at[(b / 4 * C::BN + r) * 4 + b % 4] = kb + b < KB ? srow[i][kb + b] : 127;
-            }
+            for (int b = 0; b < kScaleBlocks; ++b)
+                at[(b / 4 * C::BN + s_row) * 4 + b % 4] = kb + b < blocks_left ? srow[kb + b] : 127;
         }
+    };
+    // At the start of step s: the next kChunks, once the last chunk held is in LDS.
+    auto more_scales = [&](int s) {
+        const int c = s / kScaleSteps + 1;
+        if (s % kScaleSteps == 0 && c % kChunks == 0 && c * kScaleSteps < steps) load_scales(c);
     };
 
     // Fragments of the wave.
@@ -201,13 +212,13 @@ __global__ __launch_bounds__(C::kThreads, 2) void tiled_kernel(LinearArgs a) {
     auto load_w = [&](uint4_t (&w)[NT], float (&sc)[NT], bool& wide, int s) {
         const char* stage = lds + s % C::kStages * C::kStage;
         const int in = s % kScaleSteps;
-        const uint32_t* words = (const uint32_t*)(lds + C::kStages * C::kStage +
-                                                  (s / kScaleSteps & 1) * C::kScales);
+        const uint32_t* word = (const uint32_t*)(lds + C::kStages * C::kStage +
+                                                 (s / kScaleSteps & 1) * C::kScales);
         bool out = false;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             w[n] = *(const uint4_t*)(stage + w_at + n * kGroupBytes);
-            const uint32_t b = words[in / 2 * C::BN + wave * C::WN + 32 * n + r31] >>
+            const uint32_t b = word[in / 2 * C::BN + wave * C::WN + 32 * n + r31] >>
                                (16 * (in & 1) + 8 * half) & 255;
             out |= !f16_scale_ok(b);
             sc[n] = scale_value(b);
@@ -223,7 +234,7 @@ __global__ __launch_bounds__(C::kThreads, 2) void tiled_kernel(LinearArgs a) {
     };
 
     if (steps > 0) {
-        load_scale_chunk(0);
+        load_scales(0);
 #pragma unroll
         for (int s = 0; s < C::kStages; ++s)
             if (s < steps) copy(s);
@@ -254,8 +265,7 @@ __global__ __launch_bounds__(C::kThreads, 2) void tiled_kernel(LinearArgs a) {
         for (; s < steps; ++s) {
             if (kIsF16 && wide) break;
             const char* stage = lds + s % C::kStages * C::kStage;
-            if (s % kScaleSteps == 0 && s + kScaleSteps < steps)
-                load_scale_chunk(s / kScaleSteps + 1);
+            more_scales(s);
 #pragma unroll
             for (int i = 0; i < 3; ++i) {
                 load_x(x[(i + 1) & 1], stage, i + 1);
@@ -275,8 +285,7 @@ __global__ __launch_bounds__(C::kThreads, 2) void tiled_kernel(LinearArgs a) {
         // exact in bf16, X is the sum of two bf16 values.
         for (; kIsF16 && s < steps; ++s) {
             const char* stage = lds + s % C::kStages * C::kStage;
-            if (s % kScaleSteps == 0 && s + kScaleSteps < steps)
-                load_scale_chunk(s / kScaleSteps + 1);
+            more_scales(s);
 #pragma unroll 1
             for (int i = 0; i < 4; ++i) {
                 bf168_t w[NT];
@@ -366,9 +375,10 @@ __global__ __launch_bounds__(C::kThreads, 2) void tiled_kernel(LinearArgs a) {
     }
 }
 
-typedef Tiling<128, 64, 4, 3> Large;        // 128 x 256, two blocks a CU
-typedef Tiling<64, 64, 4, 4> Medium;        // 64 x 256, two
-typedef Tiling<64, 32, 4, 4> Small;         // 64 x 128, three
+typedef Tiling<128, 64, 4, 3, 16, 2> Large;         // 128 x 256
+typedef Tiling<64, 64, 4, 3, 8, 3> Medium;          // 64 x 256
+typedef Tiling<32, 64, 4, 4, 8, 3> Low;             // 32 x 256
+typedef Tiling<64, 32, 4, 4, 16, 3> Narrow;         // 64 x 128
 
 template <class C>
 void launch(LinearArgs a, DType dt, hipStream_t stream) {
@@ -386,35 +396,43 @@ void launch(LinearArgs a, DType dt, hipStream_t stream) {
     }
 }
 
-// Tiling and K split.
-//   Rows per expert on average (all rows of a dense product): few go to the
-//   stream kernel; many to Large, which reads each operand from LDS half as often.
-//   64 experts of 3584 x 4096, us by rows per expert (stream / Medium / Large):
-//   8: 190 / 182 / 214, 16: 285 / 178 / 261, 75: 816 / 278 / 322, 150: 1508 / 412
-//   / 446, 512: 4785 / 1115 / 1030.
-//   K slices (dense): where the tiles are fewer than what fits on 256 CUs, as
-//   many as fill them, of at least eight steps: 50 x 4096 x 14336 105 us
-//   unsplit, 24 in 8 or 16 slices; 200 rows 105 and 43 us.
+// Kernel and K split.
+//   Experts, by rows per expert on average (all rows / experts; 64 experts,
+//   gate-up 3584 x 4096 / down 4096 x 1792, us):
+//     rows       stream       Low     Medium     Large
+//     0.5       54 / 32   57 / 33    72 / 41
+//     2        117 / 63  101 / 48   111 / 56
+//     16                 144 / 70   167 / 85
+//     37                195 / 102   183 / 96
+//     150                501 / 282  356 / 219  375 / 237
+//     512              1504 / 844  1072 / 646  995 / 622
+//   Dense: the largest tiles that give every CU a block; Narrow (32 rows: Low)
+//   where none does.
+//   K slices (dense): where the tiles are fewer than the blocks that fit on 256
+//   CUs, as many as fill two a CU, of at least eight steps: 50 x 4096 x 14336
+//   105 us unsplit, 24 in 8 or 16 slices; 17 rows 30 and 20 us.
+enum Kernel { kStream, kLow, kNarrow, kMedium, kLarge };
 struct Choice {
-    int tiling;         // 0 stream, 1 large, 2 medium, 3 small
+    Kernel kernel;
     int slices, steps;
 };
-Choice choose(int64_t rows, int64_t R, int64_t N, int64_t K, bool grouped, bool split) {
+Choice choose(int64_t R, int64_t E, int64_t N, int64_t K, bool grouped, bool split) {
     const int64_t total = (K / kBlock + 1) / 2;
-    Choice c{0, 1, (int)total};
+    Choice c{kStream, 1, (int)total};
     if (grouped) {
-        c.tiling = rows < 8 ? 0 : rows <= 192 ? 2 : 1;
+        if (R >= E) c.kernel = R < 28 * E ? kLow : R < 192 * E ? kMedium : kLarge;
         return c;
     }
-    if (rows <= 16) return c;
+    if (R <= 16) return c;
     auto tiles = [&](int bm, int bn) { return (R + bm - 1) / bm * ((N + bn - 1) / bn); };
     int64_t n = tiles(128, 256);
-    c.tiling = 1;
-    if (n < 256) n = tiles(64, 256), c.tiling = 2;
-    if (n < 256) n = tiles(64, 128), c.tiling = 3;
+    c.kernel = kLarge;
+    if (n < 256) n = tiles(64, 256), c.kernel = kMedium;
+    if (n < 256) n = tiles(64, 128), c.kernel = kNarrow;
+    if (R <= 32) n = tiles(32, 256), c.kernel = kLow;
     if (split) {
-        int64_t s = 512 / n;
-        if (s > 8) s = 8;
+        int64_t s = 512 / n, most = R <= 32 ? 16 : 8;
+        if (s > most) s = most;
         if (s > total / 8) s = total / 8;
         if (s > 1) {
             c.steps = (int)((total + s - 1) / s);
@@ -428,19 +446,21 @@ Choice choose(int64_t rows, int64_t R, int64_t N, int64_t K, bool grouped, bool 
 
 size_t linear_workspace(int64_t M, int64_t N, int64_t K) {
     if (M <= 0 || N <= 0) return 0;
-    const Choice c = choose(M, M, N, K, false, true);
+    const Choice c = choose(M, 1, N, K, false, true);
     return c.slices > 1 ? (size_t)c.slices * M * N * sizeof(float) : 0;
 }
 
 hipError_t launch_linear(LinearArgs a, DType dt, float* part, hipStream_t stream) {
-    const bool grouped = a.offsets != nullptr;
-    const Choice c = choose(grouped ? a.R / a.E : a.R, a.R, a.N, a.K, grouped, part != nullptr);
+    const Choice c = choose(a.R, a.E, a.N, a.K, a.offsets != nullptr, part != nullptr);
     a.slices = c.slices, a.steps = c.steps;
     a.part = c.slices > 1 ? part : nullptr;
-    if (c.tiling == 0) return launch_stream(a, dt, stream);
-    if (c.tiling == 1) launch<Large>(a, dt, stream);
-    else if (c.tiling == 2) launch<Medium>(a, dt, stream);
-    else launch<Small>(a, dt, stream);
+    switch (c.kernel) {
+        case kStream: return launch_stream(a, dt, stream);
+        case kLow: launch<Low>(a, dt, stream); break;
+        case kNarrow: launch<Narrow>(a, dt, stream); break;
+        case kMedium: launch<Medium>(a, dt, stream); break;
+        case kLarge: launch<Large>(a, dt, stream); break;
+    }
     if (a.part) launch_add_slices(a.part, a.slices, (int64_t)a.R * a.N, a.Y, dt, stream);
     return hipGetLastError();
 }

@@ -19,6 +19,7 @@ a missing library or a non-gfx950 device is an error.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import NamedTuple
 
@@ -90,6 +91,9 @@ def _check(fn: str, status: int) -> None:
 
 
 def _need(t, name: str, dtypes, ndim: int, dense: bool = True) -> None:
+    if (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.is_cuda
+            and (not ndim or t.dim() == ndim) and (not dense or t.is_contiguous())):
+        return
     if not isinstance(t, torch.Tensor):
         raise ValueError("%s must be a torch.Tensor" % name)
     if t.dtype not in dtypes:
@@ -115,7 +119,9 @@ def _stream(*tensors) -> int:
         if t.get_device() != index:
             raise ValueError("tensors must be on the current device cuda:%d, got %s"
                              % (index, t.device))
-    return torch.cuda.current_stream(index).cuda_stream
+    # The handle alone: torch.cuda.current_stream builds a Stream object first,
+    # 1 us of the 8 a small call takes.
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
 def _row_stride(t: torch.Tensor, name: str) -> int:
@@ -130,9 +136,9 @@ def _row_stride(t: torch.Tensor, name: str) -> int:
     return t.stride(0)
 
 
-def _out(t, shape, dtype, device, name: str) -> torch.Tensor:
+def _out(t, shape, dtype, like: torch.Tensor, name: str) -> torch.Tensor:
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
     _need(t, name, (dtype,), len(shape))
     if tuple(t.shape) != tuple(shape):
         raise ValueError("%s has shape %s, want %s" % (name, tuple(t.shape), tuple(shape)))
@@ -143,11 +149,12 @@ def _weights(codes: torch.Tensor, scales: torch.Tensor, ndim: int, name: str = "
     """The shape [..., K] of an MXFP4 matrix."""
     _need(codes, name + "codes", _U8, ndim)
     _need(scales, name + "scales", _U8, ndim)
-    K = codes.shape[-1] * 2
-    if K % BLOCK or tuple(scales.shape) != tuple(codes.shape[:-1]) + (K // BLOCK,):
+    *lead, half = codes.shape
+    K = half * 2
+    if K % BLOCK or scales.shape != (*lead, K // BLOCK):
         raise ValueError("%sscales shape %s does not match %scodes %s (blocks of %d columns)"
                          % (name, tuple(scales.shape), name, tuple(codes.shape), BLOCK))
-    return tuple(codes.shape[:-1]) + (K,)
+    return (*lead, K)
 
 
 def quantize(X: torch.Tensor, codes: torch.Tensor = None, scales: torch.Tensor = None):
@@ -167,8 +174,8 @@ def quantize(X: torch.Tensor, codes: torch.Tensor = None, scales: torch.Tensor =
         _need(X, "X", _FLOATS, 0)
         rows, stride = (X.numel() // K if K else 0), K
     lead = tuple(X.shape[:-1])
-    codes = _out(codes, lead + (K // 2,), torch.uint8, X.device, "codes")
-    scales = _out(scales, lead + (K // BLOCK,), torch.uint8, X.device, "scales")
+    codes = _out(codes, lead + (K // 2,), torch.uint8, X, "codes")
+    scales = _out(scales, lead + (K // BLOCK,), torch.uint8, X, "scales")
     _check("mxfp4_quantize",
            lib.mxfp4_quantize(X.data_ptr(), _FLOATS[X.dtype], rows, K, stride, codes.data_ptr(),
                               scales.data_ptr(), _stream(X, codes, scales)))
@@ -182,7 +189,7 @@ def dequantize(codes: torch.Tensor, scales: torch.Tensor, dtype: torch.dtype = t
     if dtype not in _FLOATS:
         raise ValueError("dtype must be fp16, bf16 or fp32, got %s" % dtype)
     shape = _weights(codes, scales, 0)
-    Y = _out(Y, shape, dtype, codes.device, "Y")
+    Y = _out(Y, shape, dtype, codes, "Y")
     K = shape[-1]
     _check("mxfp4_dequantize",
            lib.mxfp4_dequantize(codes.data_ptr(), scales.data_ptr(),
@@ -191,21 +198,26 @@ def dequantize(codes: torch.Tensor, scales: torch.Tensor, dtype: torch.dtype = t
     return Y
 
 
-def _workspace(need: int, given, device, name: str):
-    """(pointer, bytes, tensor) of a workspace: the caller's, or one from
-    torch's allocator, which holds it for the current stream's order."""
+@functools.lru_cache(maxsize=4096)
+def _workspace_bytes(fn: str, a: int, b: int, c: int) -> int:
+    return getattr(library(), fn)(a, b, c)
+
+
+def _workspace(need: int, given, like: torch.Tensor):
+    """(pointer, bytes, tensors to check) of a workspace: the caller's, or one
+    from torch's allocator, which holds it for the current stream's order."""
     if given is not None:
-        _need(given, name, _U8, 1)
-        return given.data_ptr(), given.numel(), given
+        _need(given, "workspace", _U8, 1)
+        return given.data_ptr(), given.numel(), (given,)
     if need == 0:
-        return None, 0, None
-    ws = torch.empty(need, dtype=torch.uint8, device=device)
-    return ws.data_ptr(), need, ws
+        return None, 0, ()
+    ws = like.new_empty(need, dtype=torch.uint8)
+    return ws.data_ptr(), need, (ws,)
 
 
 def linear_workspace(M: int, N: int, K: int, device="cuda") -> torch.Tensor:
     """A workspace for linear() (uint8, at least 1 byte)."""
-    n = library().mxfp4_linear_workspace_bytes(M, N, K)
+    n = _workspace_bytes("mxfp4_linear_workspace_bytes", M, N, K)
     return torch.empty(max(1, n), dtype=torch.uint8, device=device)
 
 
@@ -221,19 +233,19 @@ def linear(X: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, Y: torch.
     if X.shape[1] != K:
         raise ValueError("X has %d columns, K = %d" % (X.shape[1], K))
     stride = _row_stride(X, "X")
-    Y = _out(Y, (M, N), X.dtype, X.device, "Y")
-    ws, ws_bytes, keep = _workspace(lib.mxfp4_linear_workspace_bytes(M, N, K), workspace,
-                                    X.device, "workspace")
+    Y = _out(Y, (M, N), X.dtype, X, "Y")
+    ws, ws_bytes, keep = _workspace(_workspace_bytes("mxfp4_linear_workspace_bytes", M, N, K),
+                                    workspace, X)
     _check("mxfp4_linear",
            lib.mxfp4_linear(X.data_ptr(), _HALVES[X.dtype], M, stride, codes.data_ptr(),
                             scales.data_ptr(), N, K, Y.data_ptr(), ws, ws_bytes,
-                            _stream(X, codes, scales, Y, *(() if keep is None else (keep,)))))
+                            _stream(X, codes, scales, Y, *keep)))
     return Y
 
 
 def matmul_workspace(M: int, N: int, K: int, device="cuda") -> torch.Tensor:
     """A workspace for matmul() (uint8, at least 1 byte)."""
-    n = library().mxfp4_matmul_workspace_bytes(M, N, K)
+    n = _workspace_bytes("mxfp4_matmul_workspace_bytes", M, N, K)
     return torch.empty(max(1, n), dtype=torch.uint8, device=device)
 
 
@@ -250,14 +262,14 @@ def matmul(a_codes: torch.Tensor, a_scales: torch.Tensor, b_codes: torch.Tensor,
     N, Kb = _weights(b_codes, b_scales, 2, "b_")
     if K != Kb:
         raise ValueError("A has %d columns, B has %d" % (K, Kb))
-    Y = _out(Y, (M, N), dtype, a_codes.device, "Y")
-    ws, ws_bytes, keep = _workspace(lib.mxfp4_matmul_workspace_bytes(M, N, K), workspace,
-                                    a_codes.device, "workspace")
+    Y = _out(Y, (M, N), dtype, a_codes, "Y")
+    ws, ws_bytes, keep = _workspace(_workspace_bytes("mxfp4_matmul_workspace_bytes", M, N, K),
+                                    workspace, a_codes)
     _check("mxfp4_matmul",
            lib.mxfp4_matmul(a_codes.data_ptr(), a_scales.data_ptr(), M, b_codes.data_ptr(),
                             b_scales.data_ptr(), N, K, Y.data_ptr(), _FLOATS[dtype], ws, ws_bytes,
                             _stream(a_codes, a_scales, b_codes, b_scales, Y,
-                                    *(() if keep is None else (keep,)))))
+                                    *keep)))
     return Y
 
 
@@ -275,8 +287,8 @@ def route(logits: torch.Tensor, k: int, renormalize: bool = True, ids: torch.Ten
     if not 1 <= k <= min(E, MAX_CHOICES):
         raise ValueError("k = %d, want 1 to min(%d experts, %d)" % (k, E, MAX_CHOICES))
     stride = _row_stride(logits, "logits")
-    ids = _out(ids, (T, k), torch.int32, logits.device, "ids")
-    weights = _out(weights, (T, k), torch.float32, logits.device, "weights")
+    ids = _out(ids, (T, k), torch.int32, logits, "ids")
+    weights = _out(weights, (T, k), torch.float32, logits, "weights")
     _check("moe_route",
            lib.moe_route(logits.data_ptr(), _FLOATS[logits.dtype], T, E, stride, k,
                          1 if renormalize else 0, ids.data_ptr(), weights.data_ptr(),
@@ -305,15 +317,13 @@ def plan(ids: torch.Tensor, E: int, workspace: torch.Tensor = None) -> Plan:
         raise ValueError("E = %d, want 1 to %d" % (E, MAX_EXPERTS))
     if not 1 <= k <= MAX_CHOICES:
         raise ValueError("ids have %d choices a token, want 1 to %d" % (k, MAX_CHOICES))
-    offsets = torch.empty(E + 1, dtype=torch.int32, device=ids.device)
-    tokens = torch.empty(T * k, dtype=torch.int32, device=ids.device)
-    positions = torch.empty((T, k), dtype=torch.int32, device=ids.device)
-    ws, ws_bytes, keep = _workspace(lib.moe_plan_workspace_bytes(T, k, E), workspace, ids.device,
-                                    "workspace")
+    offsets, tokens, positions = ids.new_empty(E + 1), ids.new_empty(T * k), ids.new_empty((T, k))
+    ws, ws_bytes, keep = _workspace(_workspace_bytes("moe_plan_workspace_bytes", T, k, E),
+                                    workspace, ids)
     _check("moe_plan",
            lib.moe_plan(ids.data_ptr(), T, k, E, offsets.data_ptr(), tokens.data_ptr(),
                         positions.data_ptr(), ws, ws_bytes,
-                        _stream(ids, *(() if keep is None else (keep,)))))
+                        _stream(ids, *keep)))
     return Plan(offsets, tokens, positions)
 
 
@@ -342,7 +352,7 @@ def grouped_linear(X: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
         _need(tokens, "tokens", _I32, 1)
         R = tokens.shape[0]
     stride = _row_stride(X, "X")
-    Y = _out(Y, (R, N // 2 if swiglu else N), X.dtype, X.device, "Y")
+    Y = _out(Y, (R, N // 2 if swiglu else N), X.dtype, X, "Y")
     _check("mxfp4_grouped_linear",
            lib.mxfp4_grouped_linear(X.data_ptr(), _HALVES[X.dtype], X.shape[0], stride,
                                     tokens.data_ptr() if tokens is not None else None, R,
@@ -369,7 +379,7 @@ def combine(Y: torch.Tensor, positions: torch.Tensor, weights: torch.Tensor,
     T, k = positions.shape
     if not 1 <= k <= MAX_CHOICES:
         raise ValueError("positions have %d choices a token, want 1 to %d" % (k, MAX_CHOICES))
-    out = _out(out, (T, N), Y.dtype, Y.device, "out")
+    out = _out(out, (T, N), Y.dtype, Y, "out")
     _check("moe_combine",
            lib.moe_combine(Y.data_ptr(), _HALVES[Y.dtype], R, N, positions.data_ptr(),
                            weights.data_ptr(), T, k, out.data_ptr(),
