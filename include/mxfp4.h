@@ -137,8 +137,9 @@ int moe_plan(const int32_t* ids, int64_t T, int64_t k, int64_t E, int32_t* offse
  *   tokens  in : int32 [R] or NULL (then x_rows >= R); an index outside
  *                [0, x_rows) reads a row of zeros
  *   codes, scales in: MXFP4 [E, N, K/2], [E, N, K/32]
- *   offsets in : int32 [E + 1], rising; entries outside [0, R] are clamped and
- *                a falling pair is an empty expert (never read out of bounds)
+ *   offsets in : int32 [E + 1], rising; whatever they hold, an entry counts as at
+ *                least 0 and those before it, at most R (a falling pair is an
+ *                empty expert), and every row of Y is written once
  *   Y       out: [R, N] ([R, N/2] with swiglu, N even) of X's dtype, dense;
  *                rows of no expert (before offsets[0], from offsets[E] on) are 0
  * Accuracy per h as mxfp4_linear before its rounding; Y is rounded once. */

@@ -125,21 +125,28 @@ struct Tile {
     int rows;        // rows in it (1 .. bm); 0: no tile in this slot
 };
 
-// Tiles of 64 groups, lane l holding group base + l.  Offsets are clamped to
-// [0, R], so that no value in them can lead out of bounds.
+// Tiles of 64 groups, lane l holding group base + l.  An offset counts as at
+// least 0 and the ones before it, at most R: whatever the offsets hold, the
+// groups are disjoint and cover the rows.
 struct Groups {
     int lo, hi;      // rows of this lane's group
     int first;       // tiles of the earlier lanes' groups
     int count;       // tiles of all 64
+    int end;         // where the last of them ends
 };
-__device__ __forceinline__ Groups scan_groups(const int* offsets, int E, int R, int bm, int base) {
+__device__ __forceinline__ Groups scan_groups(const int* offsets, int E, int R, int bm, int base,
+                                              int from) {
     const int lane = threadIdx.x & (kWave - 1), g = base + lane;
     Groups w;
-    w.lo = w.hi = R;
-    if (g <= E + 1) {
-        w.lo = g == 0 ? 0 : min(max(offsets[g - 1], 0), R);
-        w.hi = g == E + 1 ? R : min(max(offsets[g], w.lo), R);
+    w.hi = g <= E ? min(max(offsets[g], from), R) : R;
+#pragma unroll
+    for (int d = 1; d < kWave; d <<= 1) {
+        const int up = __shfl_up(w.hi, d);
+        if (lane >= d) w.hi = max(w.hi, up);
     }
+    w.lo = __shfl_up(w.hi, 1);
+    if (lane == 0) w.lo = from;
+    w.end = __builtin_amdgcn_readlane(w.hi, kWave - 1);
     const int tiles = (w.hi - w.lo + bm - 1) / bm;
     int sum = tiles;
 #pragma unroll
@@ -154,16 +161,20 @@ __device__ __forceinline__ Groups scan_groups(const int* offsets, int E, int R, 
 
 // Tiles in use, found by every wave for itself.
 __device__ __forceinline__ int count_tiles(const int* offsets, int E, int R, int bm) {
-    int n = 0;
-    for (int base = 0; base <= E + 1; base += kWave) n += scan_groups(offsets, E, R, bm, base).count;
+    int n = 0, from = 0;
+    for (int base = 0; base <= E + 1; base += kWave) {
+        const Groups w = scan_groups(offsets, E, R, bm, base, from);
+        n += w.count;
+        from = w.end;
+    }
     return n;
 }
 
 // Tile of a slot.
 __device__ __forceinline__ Tile find_tile(const int* offsets, int E, int R, int bm, int slot) {
-    int before = 0;
+    int before = 0, from = 0;
     for (int base = 0; base <= E + 1; base += kWave) {
-        const Groups w = scan_groups(offsets, E, R, bm, base);
+        const Groups w = scan_groups(offsets, E, R, bm, base, from);
         const int first = before + w.first;
         const int tiles = (w.hi - w.lo + bm - 1) / bm;
         const uint64_t hit = __ballot(slot >= first && slot < first + tiles);
@@ -178,6 +189,7 @@ __device__ __forceinline__ Tile find_tile(const int* offsets, int E, int R, int 
             return t;
         }
         before += w.count;
+        from = w.end;
     }
     return Tile{-1, 0, 0};
 }
