@@ -10,6 +10,13 @@
 // operands agree: half h of a wave takes block h of the step (16 bytes of
 // codes and one scale a lane), MFMA i its columns 8i .. 8i+7.
 //
+// What bounds it: the matrix cores and their feeding from LDS where tiles are
+// full (2000 x 14336 x 4096 226 us, 1.04 PFLOP/s, matrix cores 49 % busy; 4096 x
+// 16384 x 14336 1.21 PFLOP/s); with few rows the latency of a step (0.45 us of
+// LDS reads, barrier and 256 matrix-core cycles).  Blocks of 256 weight rows read
+// X from the caches least often; two or three of them a CU hide each other's
+// barriers (one of 256 x 256: 8192 tokens over 64 experts 1091 us against 1000).
+//
 // With SwiGLU a block's weight rows are 32 gate rows, their 32 up rows, the
 // next 32 gate rows ..., so that a wave holds both factors of its outputs.
 #include "mxfp4_launch.h"
