@@ -62,9 +62,11 @@ __device__ __forceinline__ float scale_value(uint32_t byte) {
 }
 
 // Eight codes (one word, column i in bits 4i..4i+3) times the scale, as eight
-// 16-bit values.  bf16 is exact for every scale (values have two mantissa
-// bits and bf16 has fp32's range); fp16 is exact for scale bytes kF16ScaleMin
-// to kF16ScaleMax (0.5 * 2^-23 = 2^-24 up to 6 * 2^13 = 49152).
+// 16-bit values.  bf16 is exact for scale bytes up to 252 (values have two
+// mantissa bits, down to the subnormal 2^-128 and up to 6 * 2^125; bytes 253 and
+// 254 give values of 2^128 and more, which pass fp32 too: quarter8 below); fp16
+// is exact for scale bytes kF16ScaleMin to kF16ScaleMax (0.5 * 2^-23 = 2^-24 up
+// to 6 * 2^13 = 49152).
 __device__ __forceinline__ bf168_t values8(uint32_t w, float s, BF16) {
     bf168_t v;
     const bf162_t a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0);
@@ -84,6 +86,20 @@ __device__ __forceinline__ half8_t values8(uint32_t w, float s, F16) {
 constexpr uint32_t kF16ScaleMin = 104, kF16ScaleMax = 140;
 __device__ __forceinline__ bool f16_scale_ok(uint32_t byte) {
     return byte - kF16ScaleMin <= kF16ScaleMax - kF16ScaleMin;
+}
+
+// A quarter of the values, exact in bf16 for every scale (2^-130 to 1.5 * 2^127):
+// a wave that met a scale byte of kFarScale or more sums its products again as
+// quarters and takes the sums times four.  Powers of two: only sums below 2^-124
+// can lose a bit (2^-148).
+constexpr uint32_t kFarScale = 253;
+__device__ __forceinline__ bf168_t quarter8(uint32_t w, uint32_t byte) {
+    bf168_t v = values8(w, scale_value(byte == 255 ? 255 : byte < 2 ? 0 : byte - 2), BF16());
+    if (byte < 2) {                     // 2^-127 is the least scale
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = (__bf16)((float)v[i] * (byte == 0 ? 0.25f : 0.5f));
+    }
+    return v;
 }
 
 // fp16 values as the exact sum of two bf16 values (11 significant bits = 8 +

@@ -52,22 +52,27 @@ __global__ __launch_bounds__(kWaves* kWave) void stream_kernel(LinearArgs a) {
 
     if (t.expert >= 0) {
         const int64_t expert_row = (int64_t)t.expert * a.N;
+        // Weight row r of tile j, and the row of X (-1: none), r = lane % 16.
+        auto weight_row = [&](int j, int r) {
+            // SwiGLU: the gate tiles, then their up tiles.
+            const bool up = a.swiglu && j >= J / 2;
+            const int col = min(col0 + kTile * (up ? j - J / 2 : j) + r, F - 1);
+            return expert_row + col + (up ? F : 0);
+        };
+        auto x_row = [&](int r) {
+            if (r >= t.rows) return -1;
+            const int src = a.tokens ? a.tokens[t.row0 + r] : t.row0 + r;
+            return src >= 0 && src < a.x_rows ? src : -1;
+        };
         const uint8_t *wc[J], *ws[J];
 #pragma unroll
         for (int j = 0; j < J; ++j) {
-            // SwiGLU: the gate tiles, then their up tiles.
-            const bool up = a.swiglu && j >= J / 2;
-            const int col = min(col0 + kTile * (up ? j - J / 2 : j) + (lane & 15), F - 1);
-            const int64_t n = expert_row + col + (up ? F : 0);
+            const int64_t n = weight_row(j, lane & 15);
             wc[j] = a.codes + n * (a.K / 2);
             ws[j] = a.scales + n * KB;
         }
-        int src = -1;
-        if ((lane & 15) < t.rows) {
-            const int r = t.row0 + (lane & 15);
-            src = a.tokens ? a.tokens[r] : r;
-        }
-        const bool live = src >= 0 && src < a.x_rows;
+        const int src = x_row(lane & 15);
+        const bool live = src >= 0;
         const uint16_t* xr = a.X + (live ? src : 0) * a.x_stride;
 
         uint4_t w[J], x[4];
@@ -121,10 +126,48 @@ __global__ __launch_bounds__(kWaves* kWave) void stream_kernel(LinearArgs a) {
             }
         };
         const int chunks = (KB + kChunkBlocks - 1) / kChunkBlocks;
+        uint64_t far = 0;               // lanes that met a scale bf16 does not hold
         load(wave);
         for (int c = wave; c < chunks; c += kWaves) {
+#pragma unroll
+            for (int j = 0; j < J; ++j) far |= __ballot(sb[j] >= kFarScale);
             multiply();
             if (c + kWaves < chunks) load(c + kWaves);
+        }
+        if (far != 0) {
+            // Weights that bf16 does not hold: the chunks again, in quarters (a test and
+            // branch in the loop costs every call 6 %: 1 x 14336 x 4096 11.15 us so, 11.8
+            // with one).  The rows are found anew, for no register to stay taken above.
+            int l = lane;
+            asm volatile("" : "+v"(l));
+            const int x_src = x_row(l & 15);
+#pragma unroll
+            for (int j = 0; j < J; ++j) acc[j] = (float4_t){0, 0, 0, 0};
+#pragma unroll 1
+            for (int i = 4 * wave; i < 4 * chunks; i += i % 4 == 3 ? 4 * kWaves - 3 : 1) {
+                const int kb = i / 4 * kChunkBlocks + (l >> 4);
+                const bool in = kb < KB;
+                uint4_t xv = {0, 0, 0, 0};
+                if (in && x_src >= 0)
+                    xv = *(const uint4_t*)(a.X + x_src * a.x_stride + (int64_t)kb * kBlock + i % 4 * 8);
+                bf168_t hi = __builtin_bit_cast(bf168_t, xv), lo;
+                if constexpr (kIsF16) split_bf16(__builtin_bit_cast(half8_t, xv), hi, lo);
+#pragma unroll
+                for (int j = 0; j < J; ++j) {
+                    const int64_t n = weight_row(j, l & 15);
+                    uint32_t word = 0, byte = 127;
+                    if (in) {
+                        word = *(const uint32_t*)(a.codes + n * (a.K / 2) + kb * 16 + i % 4 * 4);
+                        byte = a.scales[n * KB + kb];
+                    }
+                    const bf168_t q = quarter8(word, byte);
+                    acc[j] = BF16::mfma16(q, hi, acc[j]);
+                    if constexpr (kIsF16) acc[j] = BF16::mfma16(q, lo, acc[j]);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < J; ++j) acc[j] *= 4.0f;
         }
     }
 
