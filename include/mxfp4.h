@@ -50,6 +50,9 @@ extern "C" {
 #define MXFP4_BLOCK 32
 
 enum { MXFP4_FP16 = 0, MXFP4_BF16 = 1, MXFP4_FP32 = 2 };
+/* Added to the dtype of mxfp4_grouped_linear or moe_combine: the experts' rows
+ * (Y) are fp32, so that a token's sum over them is rounded once, at its end. */
+#define MXFP4_FP32_ROWS 16
 
 /* Quantize X [rows, K] (fp16, bf16 or fp32, rows `x_stride` elements apart).
  * Per block of 32 columns:
@@ -142,6 +145,8 @@ int moe_plan(const int32_t* ids, int64_t T, int64_t k, int64_t E, int32_t* offse
  *                empty expert), and every row of Y is written once
  *   Y       out: [R, N] ([R, N/2] with swiglu, N even) of X's dtype, dense;
  *                rows of no expert (before offsets[0], from offsets[E] on) are 0
+ *   dtype   X's; with MXFP4_FP32_ROWS added Y is fp32 (not with swiglu:
+ *           W4A16_ERR_INVALID_ARG)
  * Accuracy per h as mxfp4_linear before its rounding; Y is rounded once. */
 int mxfp4_grouped_linear(const void* X, int dtype, int64_t x_rows, int64_t x_stride,
                          const int32_t* tokens, int64_t R, const uint8_t* codes,
@@ -150,7 +155,9 @@ int mxfp4_grouped_linear(const void* X, int dtype, int64_t x_rows, int64_t x_str
 
 /* Weighted sum of each token's rows: out[t, n] = sum_j weights[t, j] *
  * Y[positions[t, j], n] in fp32, j rising, rounded once; a position outside
- * [0, R) adds nothing.  Y: fp16 or bf16 [R, N], out: [T, N] of that dtype. */
+ * [0, R) adds nothing.  Y: fp16 or bf16 [R, N], out: [T, N] of that dtype; with
+ * MXFP4_FP32_ROWS added to the dtype Y is fp32 (16-bit rows take half the traffic,
+ * and their own roundings make the error of out 1.4 times as large). */
 int moe_combine(const void* Y, int dtype, int64_t R, int64_t N, const int32_t* positions,
                 const float* weights, int64_t T, int64_t k, void* out, void* stream);
 

@@ -63,6 +63,12 @@ bool bad_size(int64_t n) { return n < 0 || n > kMaxSize; }
 bool bad_dtype(int dt, bool with_fp32) {
     return dt != MXFP4_FP16 && dt != MXFP4_BF16 && !(with_fp32 && dt == MXFP4_FP32);
 }
+// Takes MXFP4_FP32_ROWS out of a dtype; whether it was there.
+bool take_fp32_rows(int& dt) {
+    if (dt < MXFP4_FP32_ROWS) return false;
+    dt -= MXFP4_FP32_ROWS;
+    return true;
+}
 int elem_bytes(int dt) { return dt == MXFP4_FP32 ? 4 : 2; }
 int check_k(int64_t K) {
     if (bad_size(K)) return W4A16_ERR_INVALID_ARG;
@@ -240,19 +246,22 @@ int mxfp4_grouped_linear(const void* X, int dtype, int64_t x_rows, int64_t x_str
                          const int32_t* tokens, int64_t R, const uint8_t* codes,
                          const uint8_t* scales, const int32_t* offsets, int64_t E, int64_t N,
                          int64_t K, int swiglu, void* Y, void* stream) {
+    const bool rows32 = take_fp32_rows(dtype);
+    const int yb = rows32 ? 4 : 2;
     if (bad_dtype(dtype, false) || bad_size(x_rows) || bad_size(R) || bad_size(N) || E < 1 ||
         E > MOE_MAX_EXPERTS)
         return W4A16_ERR_INVALID_ARG;
     if (const int st = check_k(K)) return st;
     if (swiglu && N % 2) return W4A16_ERR_SHAPE;
+    if (swiglu && rows32) return W4A16_ERR_INVALID_ARG;
     if (bad_stride(x_stride, K) || (!tokens && x_rows < R)) return W4A16_ERR_INVALID_ARG;
     if (R == 0 || N == 0) return W4A16_OK;
     if (!Y || !offsets || (K > 0 && ((x_rows > 0 && !X) || !codes || !scales)))
         return W4A16_ERR_INVALID_ARG;
-    if (!aligned(X, 16) || !aligned(codes, 16) || !aligned(Y, 2) || !aligned(tokens, 4) ||
+    if (!aligned(X, 16) || !aligned(codes, 16) || !aligned(Y, yb) || !aligned(tokens, 4) ||
         !aligned(offsets, 4) || (x_rows > 1 && x_stride % 8))
         return W4A16_ERR_MISALIGNED;
-    const Span out[] = {{Y, (uint64_t)R * (swiglu ? N / 2 : N) * 2}};
+    const Span out[] = {{Y, (uint64_t)R * (swiglu ? N / 2 : N) * yb}};
     const Span in[] = {{X, span_bytes(x_rows, K, x_stride, 2)},
                        {tokens, (uint64_t)R * 4},
                        {codes, code_bytes(E * N, K)},
@@ -266,7 +275,8 @@ int mxfp4_grouped_linear(const void* X, int dtype, int64_t x_rows, int64_t x_str
     a.codes = codes;
     a.scales = scales;
     a.offsets = offsets;
-    a.Y = (uint16_t*)Y;
+    a.Y = rows32 ? nullptr : (uint16_t*)Y;
+    a.Y32 = rows32 ? (float*)Y : nullptr;
     a.x_stride = x_stride;
     a.x_rows = (int)x_rows;
     a.R = (int)R;
@@ -279,20 +289,22 @@ int mxfp4_grouped_linear(const void* X, int dtype, int64_t x_rows, int64_t x_str
 
 int moe_combine(const void* Y, int dtype, int64_t R, int64_t N, const int32_t* positions,
                 const float* weights, int64_t T, int64_t k, void* out_, void* stream) {
+    const bool rows32 = take_fp32_rows(dtype);
+    const int yb = rows32 ? 4 : 2;
     if (bad_dtype(dtype, false) || bad_size(R) || bad_size(N) || bad_size(T) || k < 1 ||
         k > MOE_MAX_CHOICES)
         return W4A16_ERR_INVALID_ARG;
     if (T == 0 || N == 0) return W4A16_OK;
     if (!out_ || !positions || !weights || (R > 0 && !Y)) return W4A16_ERR_INVALID_ARG;
-    if (!aligned(Y, 2) || !aligned(out_, 2) || !aligned(positions, 4) || !aligned(weights, 4))
+    if (!aligned(Y, yb) || !aligned(out_, 2) || !aligned(positions, 4) || !aligned(weights, 4))
         return W4A16_ERR_MISALIGNED;
     const Span out[] = {{out_, (uint64_t)T * N * 2}};
-    const Span in[] = {{Y, (uint64_t)R * N * 2}, {positions, (uint64_t)T * k * 4},
+    const Span in[] = {{Y, (uint64_t)R * N * yb}, {positions, (uint64_t)T * k * 4},
                        {weights, (uint64_t)T * k * 4}};
     if (outputs_overlap(out, in)) return W4A16_ERR_INVALID_ARG;
     if (const int st = check_device()) return st;
-    return status_of(mxfp4::launch_combine((const uint16_t*)Y, dtype_of(dtype), (int)R, (int)N,
-                                           positions, weights, (int)T, (int)k, (uint16_t*)out_,
+    return status_of(mxfp4::launch_combine(Y, rows32, dtype_of(dtype), (int)R, (int)N, positions,
+                                           weights, (int)T, (int)k, (uint16_t*)out_,
                                            stream_of(stream)));
 }
 

@@ -24,6 +24,7 @@ typedef uint32_t uint4_t __attribute__((ext_vector_type(4)));
 
 // 16-bit storage types by tag; arithmetic is always in fp32.
 struct F16 {
+    typedef uint16_t type;
     typedef half8_t vec8;
     static __device__ __forceinline__ float load(uint16_t b) {
         return (float)__builtin_bit_cast(_Float16, b);
@@ -39,6 +40,7 @@ struct F16 {
     }
 };
 struct BF16 {
+    typedef uint16_t type;
     typedef bf168_t vec8;
     static __device__ __forceinline__ float load(uint16_t b) {
         return __builtin_bit_cast(float, (uint32_t)b << 16);

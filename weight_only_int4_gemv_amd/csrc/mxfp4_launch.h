@@ -22,14 +22,15 @@ struct LinearArgs {
     const uint8_t* codes;
     const uint8_t* scales;
     const int* offsets;         // NULL: all R rows belong to expert 0
-    uint16_t* Y;
+    uint16_t* Y;                // rounded to X's type, or NULL:
+    float* Y32;                 // the rows in fp32 (not with swiglu)
     int64_t x_stride;
     int x_rows, R, E;
     int N;                      // weight rows per expert
     int K;
     int swiglu;                 // Y has N / 2 columns
     // Set by launch_linear.
-    float* part;                // fp32 partial sums [slices][R][N], or NULL
+    float* part;                // fp32 partial sums [slices][R][N], or Y32, or NULL
     int slices, steps;          // K slices, steps of a slice
     int mt, nt;                 // row tiles (dense), column blocks
     int64_t first;              // first block of this launch
@@ -65,7 +66,8 @@ hipError_t launch_route(const void* logits, DType dt, int T, int E, int64_t stri
 int64_t plan_blocks(int64_t R);          // blocks of choices; one needs no workspace
 hipError_t launch_plan(const int* ids, int R, int k, int E, int* offsets, int* tokens,
                        int* positions, int* counts, hipStream_t stream);
-hipError_t launch_combine(const uint16_t* Y, DType dt, int R, int N, const int* positions,
+// Y: fp32 (rows32) or dt.
+hipError_t launch_combine(const void* Y, bool rows32, DType dt, int R, int N, const int* positions,
                           const float* weights, int T, int k, uint16_t* out, hipStream_t stream);
 
 }  // namespace mxfp4

@@ -188,7 +188,9 @@ __global__ __launch_bounds__(kWaves* kWave) void stream_kernel(LinearArgs a) {
             if (J > 1 && a.swiglu) h[1] += part[v][j0 + J / 2][r][n % kTile];
         }
         const float y = a.swiglu ? silu(h[0]) * h[1] : h[0];
-        a.Y[(int64_t)(t.row0 + r) * F + col0 + n] = T::store(y);
+        const int64_t at = (int64_t)(t.row0 + r) * F + col0 + n;
+        if (a.part != nullptr) a.part[at] = y;
+        else a.Y[at] = T::store(y);
     }
 }
 

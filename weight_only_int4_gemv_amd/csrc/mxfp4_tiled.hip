@@ -393,7 +393,7 @@ __global__ __launch_bounds__(C::kThreads, C::kPerCu * C::kWaves / 4) void tiled_
         const int64_t out0 = (int64_t)(t.row0 + 32 * m) * F + wcol0;
         if (a.part != nullptr) {
             float* p = a.part + (int64_t)slice * a.R * F + out0;
-            if (F % 4 == 0) {
+            if (F % 4 == 0 && (uintptr_t)a.part % 16 == 0) {
                 for (int i = lane; i < 32 * C::WN / 4; i += kWave) {
                     const int r = i / (C::WN / 4), c = i % (C::WN / 4) * 4;
                     if (r < rows && c < cols)
@@ -505,7 +505,7 @@ size_t linear_workspace(int64_t M, int64_t N, int64_t K) {
 hipError_t launch_linear(LinearArgs a, DType dt, float* part, hipStream_t stream) {
     const Choice c = choose(a.R, a.E, a.N, a.K, a.offsets != nullptr, part != nullptr);
     a.slices = c.slices, a.steps = c.steps;
-    a.part = c.slices > 1 ? part : nullptr;
+    a.part = c.slices > 1 ? part : a.Y32;
     switch (c.kernel) {
         case kStream: return launch_stream(a, dt, stream);
         case kLow: launch<Low>(a, dt, stream); break;
@@ -513,7 +513,7 @@ hipError_t launch_linear(LinearArgs a, DType dt, float* part, hipStream_t stream
         case kMedium: launch<Medium>(a, dt, stream); break;
         case kLarge: launch<Large>(a, dt, stream); break;
     }
-    if (a.part) launch_add_slices(a.part, a.slices, (int64_t)a.R * a.N, a.Y, dt, stream);
+    if (c.slices > 1) launch_add_slices(a.part, a.slices, (int64_t)a.R * a.N, a.Y, dt, stream);
     return hipGetLastError();
 }
 

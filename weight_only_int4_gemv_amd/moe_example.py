@@ -29,8 +29,8 @@ class Layer:
         ids, weights = mxfp4.route(logits, self.choices)
         p = mxfp4.plan(ids, self.experts)
         h = mxfp4.grouped_linear(x, *self.gate_up, p.offsets, tokens=p.tokens, swiglu=True)
-        y = mxfp4.grouped_linear(h, *self.down, p.offsets)
-        return mxfp4.combine(y, p.positions, weights)
+        y = mxfp4.grouped_linear(h, *self.down, p.offsets, dtype=torch.float32)
+        return mxfp4.combine(y, p.positions, weights, dtype=x.dtype)
 
 
 def reference(layer: Layer, x: torch.Tensor) -> torch.Tensor:

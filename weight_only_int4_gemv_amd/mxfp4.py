@@ -13,8 +13,8 @@ a missing library or a non-gfx950 device is an error.
     ids, weights = route(logits, k)             # logits [T, E]
     p = plan(ids, E)                            # rows ordered by expert
     H = grouped_linear(X, c1, s1, p.offsets, tokens=p.tokens, swiglu=True)
-    H = grouped_linear(H, c2, s2, p.offsets)
-    out = combine(H, p.positions, weights)      # [T, N]
+    H = grouped_linear(H, c2, s2, p.offsets, dtype=torch.float32)
+    out = combine(H, p.positions, weights, dtype=X.dtype)       # [T, N]
 """
 from __future__ import annotations
 
@@ -32,6 +32,7 @@ MAX_EXPERTS = 1024
 MAX_CHOICES = 32
 _FLOATS = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
 _HALVES = {torch.float16: 0, torch.bfloat16: 1}
+_FP32_ROWS = 16                  # added to a dtype: the experts' rows are fp32
 
 _p = ctypes.c_void_p
 _i64 = ctypes.c_int64
@@ -329,12 +330,13 @@ def plan(ids: torch.Tensor, E: int, workspace: torch.Tensor = None) -> Plan:
 
 def grouped_linear(X: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
                    offsets: torch.Tensor, tokens: torch.Tensor = None, swiglu: bool = False,
-                   Y: torch.Tensor = None) -> torch.Tensor:
+                   Y: torch.Tensor = None, dtype: torch.dtype = None) -> torch.Tensor:
     """Row r of Y = its row of X (tokens[r], or r) times the MXFP4 weights
     [E, N, K] of the expert e with offsets[e] <= r < offsets[e + 1]; rows of no
     expert are 0.  Y is [R, N] of X's dtype, R = len(tokens) or X's rows.
     swiglu: the weights are gate rows, then up rows, and Y = silu(gate) * up
-    is [R, N / 2]."""
+    is [R, N / 2].  dtype: Y's, X's (the default) or, without swiglu, fp32, for
+    combine to round a token's sum once."""
     lib = library()
     E, N, K = _weights(codes, scales, 3)
     _need(X, "X", _HALVES, 2, dense=False)
@@ -344,6 +346,10 @@ def grouped_linear(X: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
         raise ValueError("codes hold %d experts, want 1 to %d" % (E, MAX_EXPERTS))
     if swiglu and N % 2:
         raise ValueError("swiglu takes an even number of weight rows, got %d" % N)
+    if dtype not in (None, X.dtype) and (swiglu or dtype != torch.float32):
+        raise ValueError("dtype must be %s%s, got %s"
+                         % (X.dtype, "" if swiglu else " or torch.float32", dtype))
+    rows32 = dtype == torch.float32
     _need(offsets, "offsets", _I32, 1)
     if offsets.shape[0] != E + 1:
         raise ValueError("offsets has %d entries, want %d" % (offsets.shape[0], E + 1))
@@ -352,9 +358,10 @@ def grouped_linear(X: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
         _need(tokens, "tokens", _I32, 1)
         R = tokens.shape[0]
     stride = _row_stride(X, "X")
-    Y = _out(Y, (R, N // 2 if swiglu else N), X.dtype, X, "Y")
+    Y = _out(Y, (R, N // 2 if swiglu else N), dtype or X.dtype, X, "Y")
     _check("mxfp4_grouped_linear",
-           lib.mxfp4_grouped_linear(X.data_ptr(), _HALVES[X.dtype], X.shape[0], stride,
+           lib.mxfp4_grouped_linear(X.data_ptr(), _HALVES[X.dtype] + (_FP32_ROWS if rows32 else 0),
+                                    X.shape[0], stride,
                                     tokens.data_ptr() if tokens is not None else None, R,
                                     codes.data_ptr(), scales.data_ptr(), offsets.data_ptr(), E, N,
                                     K, 1 if swiglu else 0, Y.data_ptr(),
@@ -364,12 +371,18 @@ def grouped_linear(X: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
 
 
 def combine(Y: torch.Tensor, positions: torch.Tensor, weights: torch.Tensor,
-            out: torch.Tensor = None) -> torch.Tensor:
+            out: torch.Tensor = None, dtype: torch.dtype = None) -> torch.Tensor:
     """out[t] = sum over j of weights[t, j] * Y[positions[t, j]] (fp32 sums, j
-    rising; a position outside Y adds nothing): Y fp16 or bf16 [R, N], positions
-    int32 and weights fp32 [T, k] -> [T, N] of Y's dtype."""
+    rising; a position outside Y adds nothing): Y fp16, bf16 or fp32 [R, N],
+    positions int32 and weights fp32 [T, k] -> [T, N] of Y's dtype, for fp32 Y of
+    dtype (fp16 or bf16)."""
     lib = library()
-    _need(Y, "Y", _HALVES, 2)
+    _need(Y, "Y", _FLOATS, 2)
+    rows32 = Y.dtype == torch.float32
+    dtype = dtype or Y.dtype
+    if dtype not in _HALVES or not rows32 and dtype != Y.dtype:
+        raise ValueError("dtype must be %s, got %s"
+                         % ("fp16 or bf16 for fp32 Y" if rows32 else Y.dtype, dtype))
     _need(positions, "positions", _I32, 2)
     _need(weights, "weights", _F32, 2)
     if positions.shape != weights.shape:
@@ -379,9 +392,9 @@ def combine(Y: torch.Tensor, positions: torch.Tensor, weights: torch.Tensor,
     T, k = positions.shape
     if not 1 <= k <= MAX_CHOICES:
         raise ValueError("positions have %d choices a token, want 1 to %d" % (k, MAX_CHOICES))
-    out = _out(out, (T, N), Y.dtype, Y, "out")
+    out = _out(out, (T, N), dtype, Y, "out")
     _check("moe_combine",
-           lib.moe_combine(Y.data_ptr(), _HALVES[Y.dtype], R, N, positions.data_ptr(),
-                           weights.data_ptr(), T, k, out.data_ptr(),
+           lib.moe_combine(Y.data_ptr(), _HALVES[dtype] + (_FP32_ROWS if rows32 else 0), R, N,
+                           positions.data_ptr(), weights.data_ptr(), T, k, out.data_ptr(),
                            _stream(Y, positions, weights, out)))
     return out
