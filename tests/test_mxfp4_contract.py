@@ -1,10 +1,13 @@
 """What include/mxfp4.h promises, on the host: refusals of the entry points that
 test_mxfp4_host does not reach (no kernel is launched)."""
+import os
+import re
+
 import pytest
 import torch
 
 from test_mxfp4_host import A, B, C, D, DEVICE, F, INVALID, MISALIGNED, OK, lib  # noqa: F401
-from weight_only_int4_gemv_amd import mxfp4
+from weight_only_int4_gemv_amd import build
 
 ROWS = 16                            # MXFP4_FP32_ROWS
 no_gpu = pytest.mark.skipif(torch.cuda.is_available(), reason="the addresses are not real")
@@ -36,3 +39,17 @@ def test_fp32_rows_reach_the_device_check(lib):  # noqa: F811
         assert grouped(lib, dt) == DEVICE and combine(lib, dt) == DEVICE
         assert grouped(lib, dt, Y=F + 4) == DEVICE and combine(lib, dt, Y=A + 4) == DEVICE
         assert combine(lib, dt, out=A + 128) == DEVICE
+
+
+# ------------------------------------------------------------- inline assembly
+
+def test_assembly_names_the_registers_it_writes():
+    """Every asm block that moves a value into m0 says so to the compiler."""
+    found = 0
+    for name in os.listdir(build.CSRC):
+        text = open(os.path.join(build.CSRC, name)).read()
+        for block in re.findall(r"asm volatile\((.*?)\);", text, re.S):
+            if "s_mov_b32 m0" in block:
+                found += 1
+                assert '"m0"' in block.rsplit(":", 1)[1], (name, block)
+    assert found >= 2

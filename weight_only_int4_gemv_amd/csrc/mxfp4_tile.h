@@ -28,14 +28,14 @@ __device__ __forceinline__ void copy16(uint4_t rsrc, uint32_t voff, uint32_t sof
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                  :
                  : "s"(lds), "v"(voff), "s"(rsrc), "s"(soff)
-                 : "memory");
+                 : "m0", "memory");
 }
 // The same from a 64-bit address per lane.
 __device__ __forceinline__ void copy16(const void* p, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, off"
                  :
                  : "s"(lds), "v"(p)
-                 : "memory");
+                 : "m0", "memory");
 }
 // Waits until at most `left` of the wave's loads are in flight and its LDS
 // operations are done, then for the block's other waves.
