@@ -29,8 +29,9 @@
  *     nothing (its pointers may then be NULL).  K == 0 makes every output of
  *     a product 0 (inputs without elements may be NULL).
  *   - Row strides count elements, at least K (else W4A16_ERR_INVALID_ARG).
- *   - Alignment: X, its row stride in bytes and codes 16; other tensors their
- *     element size (else W4A16_ERR_MISALIGNED).
+ *   - Alignment: X, its row stride in bytes, codes and the Y of
+ *     mxfp4_dequantize 16; other tensors their element size (else
+ *     W4A16_ERR_MISALIGNED).
  *   - Outputs must not overlap inputs or each other (W4A16_ERR_INVALID_ARG).
  *   - Infinities and NaN are legal in every floating point input.
  *   - The current HIP device must be gfx950 (W4A16_ERR_DEVICE).

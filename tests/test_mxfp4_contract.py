@@ -6,8 +6,8 @@ import re
 import pytest
 import torch
 
-from test_mxfp4_host import A, B, C, D, DEVICE, F, INVALID, MISALIGNED, OK, lib  # noqa: F401
-from weight_only_int4_gemv_amd import build
+from test_mxfp4_host import A, B, C, D, DEVICE, F, INVALID, MISALIGNED, OK, ROOT, lib  # noqa: F401
+from weight_only_int4_gemv_amd import build, mxfp4
 
 ROWS = 16                            # MXFP4_FP32_ROWS
 no_gpu = pytest.mark.skipif(torch.cuda.is_available(), reason="the addresses are not real")
@@ -53,3 +53,26 @@ def test_assembly_names_the_registers_it_writes():
                 found += 1
                 assert '"m0"' in block.rsplit(":", 1)[1], (name, block)
     assert found >= 2
+
+
+# ------------------------------------------------------------------- alignment
+
+def words(*path):
+    text = open(os.path.join(ROOT, *path)).read()
+    return " ".join(re.sub(r"^\s*[*#/]+", "", text, flags=re.M).split())
+
+
+@no_gpu
+def test_dequantize_alignment_is_as_documented(lib):  # noqa: F811
+    """Y of mxfp4_dequantize takes 16 bytes, as X and the codes do; the outputs of the
+    other entry points their element size."""
+    assert "X, its row stride in bytes, codes and the Y of mxfp4_dequantize 16" in \
+        words("include", "mxfp4.h")
+    assert "Y starts on 16 bytes" in " ".join(mxfp4.dequantize.__doc__.split())
+    for dt, size in ((0, 2), (1, 2), (2, 4)):
+        for at in (size, 8):
+            assert lib.mxfp4_dequantize(A, B, 4, 64, C + at, dt, None) == MISALIGNED
+        assert lib.mxfp4_dequantize(A, B, 4, 64, C + 16, dt, None) == DEVICE
+    assert lib.mxfp4_linear(A, 1, 4, 64, B, C, 8, 64, D + 2, None, 0, None) == DEVICE
+    assert lib.mxfp4_matmul(A, B, 4, C, D, 8, 64, F + 4, 2, None, 0, None) == DEVICE
+    assert lib.moe_combine(A + 2, 0, 4, 8, B, C, 2, 2, D + 2, None) == DEVICE

@@ -185,7 +185,8 @@ def quantize(X: torch.Tensor, codes: torch.Tensor = None, scales: torch.Tensor =
 
 def dequantize(codes: torch.Tensor, scales: torch.Tensor, dtype: torch.dtype = torch.bfloat16,
                Y: torch.Tensor = None) -> torch.Tensor:
-    """The values of MXFP4 codes and scales, [..., K] of dtype (fp16, bf16, fp32)."""
+    """The values of MXFP4 codes and scales, [..., K] of dtype (fp16, bf16, fp32).
+    Y starts on 16 bytes."""
     lib = library()
     if dtype not in _FLOATS:
         raise ValueError("dtype must be fp16, bf16 or fp32, got %s" % dtype)
