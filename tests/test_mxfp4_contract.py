@@ -76,3 +76,11 @@ def test_dequantize_alignment_is_as_documented(lib):  # noqa: F811
     assert lib.mxfp4_linear(A, 1, 4, 64, B, C, 8, 64, D + 2, None, 0, None) == DEVICE
     assert lib.mxfp4_matmul(A, B, 4, C, D, 8, 64, F + 4, 2, None, 0, None) == DEVICE
     assert lib.moe_combine(A + 2, 0, 4, 8, B, C, 2, 2, D + 2, None) == DEVICE
+
+
+def test_every_vector_type_is_used():
+    sources = "".join(open(os.path.join(build.CSRC, n)).read() for n in os.listdir(build.CSRC)
+                      if n.startswith(("mxfp4", "moe")))
+    types = re.findall(r"typedef \w+ (\w+) __attribute__", sources)
+    assert len(types) > 5
+    assert [t for t in types if len(re.findall(r"\b%s\b" % t, sources)) < 2] == []

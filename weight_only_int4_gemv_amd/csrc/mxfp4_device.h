@@ -17,7 +17,6 @@ typedef __bf16 bf168_t __attribute__((ext_vector_type(8)));
 typedef float float2_t __attribute__((ext_vector_type(2)));
 typedef float float4_t __attribute__((ext_vector_type(4)));
 typedef float float16_t __attribute__((ext_vector_type(16)));
-typedef int int4_t __attribute__((ext_vector_type(4)));
 typedef int int8_t_ __attribute__((ext_vector_type(8)));
 typedef uint32_t uint2_t __attribute__((ext_vector_type(2)));
 typedef uint32_t uint4_t __attribute__((ext_vector_type(4)));

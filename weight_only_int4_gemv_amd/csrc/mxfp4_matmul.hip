@@ -62,19 +62,19 @@ struct Out<kF16> {
 
 constexpr int kScaleBlocks = 16;        // blocks of a row whose scales are staged together
 
-template <int BM_, int BN_, int WM_, int WN_, int STEP, int STAGES>
+template <int BM_, int BN_, int WM_, int WN_, int STAGES>
 struct Tiling {
     static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;
-    static constexpr int kStep = STEP, kStages = STAGES;
+    static constexpr int kStep = 8, kStages = STAGES;
     static constexpr int kWavesN = BN / WN, kWaves = BM / WM * kWavesN, kThreads = kWaves * kWave;
     static constexpr int kRows = BM + BN;                   // A rows, then B rows
-    static constexpr int kRowBytes = STEP * 16;
+    static constexpr int kRowBytes = kStep * 16;
     static constexpr int kStage = kRows * kRowBytes;
     static constexpr int kScales = kRows * kScaleBlocks;
     static constexpr int kRowsPerCopy = 1024 / kRowBytes;   // rows of one wave's copy
     static constexpr int kCopyRows = kRowsPerCopy * kWaves; // of one copy of every wave
     static constexpr int kCopies = kRows / kCopyRows;
-    static constexpr int kScaleSteps = kScaleBlocks / STEP;
+    static constexpr int kScaleSteps = kScaleBlocks / kStep;
     static constexpr int kScaleRows = (kRows + kThreads - 1) / kThreads;
     static constexpr int kLds = STAGES * kStage + 2 * kScales;
     static constexpr int kWaveLds = kLds / kWaves / 16 * 16;      // a wave's share in the epilogue
@@ -82,7 +82,7 @@ struct Tiling {
     static_assert(kCopyRows % 16 == 0, "copies of a lane share its place in the swizzle");
     // Where 16-byte chunk c of a row stands: c ^ swizzle(row).
     static __device__ __forceinline__ int swizzle(int row) {
-        return (STEP == 8 ? row >> 1 : row >> 2) & (STEP - 1);
+        return (row >> 1) & (kStep - 1);
     }
 };
 
@@ -159,7 +159,7 @@ __global__ __launch_bounds__(T::kThreads) void matmul_kernel(MatmulArgs a) {
         for (int c = 0; c < T::kCopies; ++c) {
             const int row = c * T::kCopyRows;
             const uint32_t from = (uint32_t)(row < T::BM ? row : row - T::BM) * row_bytes;
-            copy16(row < T::BM ? arsrc : brsrc, voff + from, 0, to + row * T::kRowBytes);
+            copy16(row < T::BM ? arsrc : brsrc, voff + from, to + row * T::kRowBytes);
         }
         voff += T::kRowBytes;
     };
@@ -229,17 +229,12 @@ __global__ __launch_bounds__(T::kThreads) void matmul_kernel(MatmulArgs a) {
         const char* stage = lds + s % T::kStages * T::kStage;
         const uint32_t* scales = (const uint32_t*)(lds + T::kStages * T::kStage + (sc & 1) * T::kScales);
         uint32_t sa[T::WM / 32], sb[T::WN / 32];
-        const int word = T::kStep == 8 ? in_sc * 2 + half : in_sc;
+        const int word = in_sc * 2 + half;
 #pragma unroll
-        for (int m = 0; m < T::WM / 32; ++m) {
-            sa[m] = scales[word * T::kRows + wm + 32 * m + r31];
-            if (T::kStep == 4) sa[m] >>= 16 * half;
-        }
+        for (int m = 0; m < T::WM / 32; ++m) sa[m] = scales[word * T::kRows + wm + 32 * m + r31];
 #pragma unroll
-        for (int n = 0; n < T::WN / 32; ++n) {
+        for (int n = 0; n < T::WN / 32; ++n)
             sb[n] = scales[word * T::kRows + T::BM + wn + 32 * n + r31];
-            if (T::kStep == 4) sb[n] >>= 16 * half;
-        }
         const char* ar = stage + (wm + r31) * T::kRowBytes;
         const char* br = stage + (T::BM + wn + r31) * T::kRowBytes;
         Fragments<T> f;
@@ -341,9 +336,9 @@ void add_slices(const float* part, int slices, int64_t n, void* Y, hipStream_t s
     else add_slices_kernel<DT, 1><<<grid, 256, 0, stream>>>(part, slices, n, (out_t*)Y);
 }
 
-typedef Tiling<256, 256, 128, 64, 8, 2> Large;     // one block a CU
-typedef Tiling<128, 128, 64, 64, 8, 2> Medium;     // two
-typedef Tiling<64, 64, 32, 32, 8, 4> Small;        // two
+typedef Tiling<256, 256, 128, 64, 2> Large;     // one block a CU
+typedef Tiling<128, 128, 64, 64, 2> Medium;     // two
+typedef Tiling<64, 64, 32, 32, 4> Small;        // two
 
 // Tiling and K split, by how the output tiles fill 256 CUs.
 //   Large against Medium: a round of 256 large tiles takes 5/3 of the time of a

@@ -18,16 +18,16 @@ __device__ __forceinline__ uint4_t make_rsrc(const void* p, uint32_t bytes) {
     return (uint4_t){(uint32_t)b, (uint32_t)(b >> 32) & 0xFFFFu, bytes, 0x00020000u};
 }
 
-// 16 bytes per lane from rsrc base + voff + soff into LDS at lds + 16 * lane
-// (lds, rsrc and soff the same in the wave).  No register is written: the copy
+// 16 bytes per lane from rsrc base + voff into LDS at lds + 16 * lane (lds and
+// rsrc the same in the wave).  No register is written: the copy
 // is complete once the wave's load counter has passed it (wait_copies).
 // Written as assembly because the compiler waits for every such copy in flight
 // before any LDS read.  The five wait states are those between a lane-read
 // SGPR and a memory instruction that uses it.
-__device__ __forceinline__ void copy16(uint4_t rsrc, uint32_t voff, uint32_t soff, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+__device__ __forceinline__ void copy16(uint4_t rsrc, uint32_t voff, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                  :
-                 : "s"(lds), "v"(voff), "s"(rsrc), "s"(soff)
+                 : "s"(lds), "v"(voff), "s"(rsrc)
                  : "m0", "memory");
 }
 // The same from a 64-bit address per lane.

@@ -158,7 +158,7 @@ __global__ __launch_bounds__(C::kThreads, C::kPerCu * C::kWaves / 4) void tiled_
         // Blocks past K are the next row's first codes (or 0): they meet zeros.
 #pragma unroll
         for (int j = 0; j < C::kWCopies; ++j)
-            copy16(wrsrc[j], w_off, 0, to + C::kXBytes + (j * C::kWaves + wave) * kGroupBytes);
+            copy16(wrsrc[j], w_off, to + C::kXBytes + (j * C::kWaves + wave) * kGroupBytes);
         w_off += kStepCols / 2;
     };
 
