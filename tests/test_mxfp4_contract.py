@@ -84,3 +84,33 @@ def test_every_vector_type_is_used():
     types = re.findall(r"typedef \w+ (\w+) __attribute__", sources)
     assert len(types) > 5
     assert [t for t in types if len(re.findall(r"\b%s\b" % t, sources)) < 2] == []
+
+
+# ------------------------------------------------------------------ workspaces
+
+@no_gpu
+@pytest.mark.parametrize("name", ["linear", "matmul"])
+def test_workspace_rules(lib, name):  # noqa: F811
+    """Where K is split: too few bytes, memory off 16 bytes or over another tensor are
+    refused, NULL and larger memory are not."""
+    M, N, K = 50, 512, 8192
+    need = getattr(lib, "mxfp4_%s_workspace_bytes" % name)(M, N, K)
+    assert need > 0 and need % (M * N * 4) == 0
+    far = 8 * F
+
+    def call(ws, bytes_):
+        if name == "linear":
+            return lib.mxfp4_linear(A, 0, M, K, B, C, N, K, D, ws, bytes_, None)
+        return lib.mxfp4_matmul(A, B, M, C, D, N, K, F, 0, ws, bytes_, None)
+    assert call(far, need) == DEVICE and call(far, need + 5) == DEVICE and call(None, 0) == DEVICE
+    assert call(far, need - 1) == INVALID and call(far, 0) == INVALID and call(None, need) == INVALID
+    assert call(far + 8, need) == MISALIGNED
+    for other in (A, B, C, D):
+        assert call(other + 16, need) == INVALID and call(other - need + 16, need) == INVALID
+
+
+def test_sizes_out_of_range_need_no_workspace(lib):  # noqa: F811
+    for fn in (lib.mxfp4_linear_workspace_bytes, lib.mxfp4_matmul_workspace_bytes):
+        for M, N, K in ((-1, 8, 32), (8, -1, 32), (8, 8, -32), (8, 8, 33), (1 << 25, 8, 32),
+                        (8, 1 << 25, 32), (8, 8, 1 << 25), (0, 8, 64), (8, 0, 64), (8, 8, 0)):
+            assert fn(M, N, K) == 0
