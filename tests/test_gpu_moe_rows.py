@@ -119,3 +119,26 @@ def test_dtype_refusals(mx):  # noqa: F811
                  lambda: mx.combine(y32, pos, w, dtype=x.dtype, out=y32[:1])):
         with pytest.raises(ValueError):
             call()
+
+
+@pytest.mark.parametrize("T", [1, 16, 300])
+def test_example_router_is_not_quantized(T):
+    """The example's layer takes the experts that its router, as given, chooses."""
+    from weight_only_int4_gemv_amd import moe_example, mxfp4
+    say("example router T=%d" % T)
+    rng = np.random.default_rng(T)
+    E, K, F = 16, 256, 32
+    router = gpu(rng.standard_normal((E, K)) / K ** 0.5, torch.bfloat16)
+    layer = moe_example.Layer(gpu(rng.standard_normal((E, 2 * F, K)), torch.bfloat16),
+                              gpu(rng.standard_normal((E, K, F)), torch.bfloat16), router, 3)
+    x = gpu(rng.standard_normal((T, K)), torch.bfloat16)
+    logits = layer.logits(x)
+    want, mags = ref.product(ref.f64(x), ref.f64(router))
+    # fp32 sums of any order: a rounding for each product and sum
+    bound = K * 2.0 ** -23 * mags
+    assert (np.abs(ref.f64(logits) - want) <= bound).all()
+    ids, weights = mxfp4.route(logits, 3)
+    want_ids, want_weights = ref.route(want, 3, True)
+    assert np.array_equal(ids.cpu().numpy(), want_ids)
+    # |dw| <= 2 w (1 - w) max |dl| for a softmax, whose own terms are a few units off
+    assert np.abs(ref.f64(weights) - want_weights).max() <= bound.max() / 2 + 2.0 ** -20

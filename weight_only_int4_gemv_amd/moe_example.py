@@ -1,7 +1,9 @@
 """One mixture-of-experts feed-forward layer with MXFP4 experts, as a serving
-loop runs it: weights quantized once, then per step routing, the expert-ordered
-plan, the gathered gate-up product with silu(gate) * up, the down product and
-the weighted sum, seven launches that replay from one graph.
+loop runs it: the experts' weights quantized once (the router keeps its own, a
+small matrix whose rounding would change which experts run), then per step the
+router's product, routing, the expert-ordered plan, the gathered gate-up product
+with silu(gate) * up, the down product and the weighted sum, replayed from one
+graph.
 
     python -m weight_only_int4_gemv_amd.moe_example [tokens]
 """
@@ -16,17 +18,19 @@ from . import mxfp4
 
 
 class Layer:
-    """E experts of `inner` gate and up rows over `hidden` columns."""
+    """E experts of `inner` gate and up rows over `hidden` columns; router [E, hidden]."""
 
     def __init__(self, gate_up: torch.Tensor, down: torch.Tensor, router: torch.Tensor, choices: int):
         self.gate_up = mxfp4.quantize(gate_up)       # [E, 2 inner, hidden]
         self.down = mxfp4.quantize(down)             # [E, hidden, inner]
-        self.router = mxfp4.quantize(router)         # [E, hidden]
+        self.router = router.float()
         self.experts, self.choices = gate_up.shape[0], choices
 
+    def logits(self, x: torch.Tensor) -> torch.Tensor:
+        return torch.nn.functional.linear(x.float(), self.router)
+
     def __call__(self, x: torch.Tensor) -> torch.Tensor:
-        logits = mxfp4.linear(x, *self.router)
-        ids, weights = mxfp4.route(logits, self.choices)
+        ids, weights = mxfp4.route(self.logits(x), self.choices)
         p = mxfp4.plan(ids, self.experts)
         h = mxfp4.grouped_linear(x, *self.gate_up, p.offsets, tokens=p.tokens, swiglu=True)
         y = mxfp4.grouped_linear(h, *self.down, p.offsets, dtype=torch.float32)
@@ -34,11 +38,11 @@ class Layer:
 
 
 def reference(layer: Layer, x: torch.Tensor) -> torch.Tensor:
-    """The layer in 64 bits on the values its codes stand for; the experts are
-    chosen by the layer's own router logits."""
+    """The layer in 64 bits, its router too, on the values the experts' codes stand
+    for."""
     value = [mxfp4.dequantize(c, s, dtype=torch.float32).double().cpu()
              for c, s in (layer.gate_up, layer.down)]
-    logits = mxfp4.linear(x, *layer.router).double().cpu()
+    logits = x.double().cpu() @ layer.router.double().cpu().t()
     top, ids = torch.sort(logits, dim=1, descending=True, stable=True)
     weights = torch.softmax(top[:, :layer.choices], dim=1)
     out = torch.zeros(x.shape, dtype=torch.float64)
