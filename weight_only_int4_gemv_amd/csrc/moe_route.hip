@@ -11,9 +11,11 @@ namespace {
 // One wave per token; lane l holds the logits l, l + 64, ...  A choice is the
 // largest key over the wave: the logit mapped to an unsigned number in its
 // order (a NaN above everything, -infinity lowest), then the lower expert.
-// Latency bounds it: the maximum is taken between lanes' registers (DPP) and the
-// expert found by comparing with it, without a trip through LDS (8191 tokens,
-// 8 of 128 experts: 8.3 us, with 64-bit shuffles 13.5).
+// The maximum is taken between lanes' registers (DPP) and the expert found by
+// comparing with it, without a trip through LDS.  Three tokens: 2.4 us, the latency
+// of a launch.  Many tokens are bound by instruction issue: 8191 tokens, 8 of 128
+// experts, 8.2 us (with 64-bit shuffles 13.5) are eight waves on every SIMD of 428
+// vector instructions each, 14 of the launch's 20 thousand cycles; 2^20 tokens 510 us.
 
 template <DType DT>
 __device__ __forceinline__ float logit(const void* p, int64_t i) {
@@ -123,7 +125,9 @@ void route(const void* logits, int T, int E, int64_t stride, int k, bool renorm,
 // then each block forms its own bucket starts from all counts, and each wave
 // ranks its choices 64 at a time, in order.  Integer sums only: the result
 // does not depend on scheduling.
-// Latency bounds it: 24 choices of 64 experts 3.3 us, 65528 of 128 in 5 + 10 us.
+// Latency bounds it: 18 choices of 64 experts 3.4 us, 65528 of 128 in 5 + 10 us on
+// 16 blocks.  Every block reads all counts, so the time grows with the square of the
+// blocks in the end: 2^20 choices 27 us, 2^23 217 us, 2^24 (of 64 experts) 690 us.
 
 constexpr int kPlanThreads = 512;
 constexpr int kPlanWaves = kPlanThreads / kWave;

@@ -10,8 +10,10 @@
 // neighbours (one word, its byte chosen by the instruction).
 //
 // What bounds it: copies to LDS and matrix instructions, 443 us each alone of the
-// 590 that 4096 x 28672 x 8192 takes (3.3 PFLOP/s, matrix cores 39 % busy); with
-// few rows the latency of a step (1.4 us, one tile copy on its way).
+// 546 that 4096 x 28672 x 8192 takes in a row of calls (3.5 PFLOP/s; 575-590 us
+// and matrix cores 39 % busy in traced launches): they run largely in turn, since
+// every wave waits for a whole stage at one barrier.  With few rows the latency of
+// a step (1.4 us): one block a CU with one tile copy on its way.
 //
 // A block of BM x BN outputs walks K in steps of kStep blocks.  Code tiles go
 // from global memory straight to LDS, kStages tiles deep; scales, 16 blocks of

@@ -4,7 +4,8 @@
 // to the nearest e2m1 value (ties to even, saturated at 6).  The division by a
 // power of two is exact, so the rounding is one instruction per two elements
 // (the scaled fp4 conversions); what bounds both kernels is memory: 28672 x 8192
-// fp16 in 122 us (4.9 TB/s) and back in 97 us (6.1 TB/s), one pass each.
+// fp16 in 122 us (4.9 TB/s) and back in 97 us (6.1 TB/s; of its 595 MB the 125 MB of
+// codes were just written and may come from the last-level cache), one pass each.
 #include "mxfp4_device.h"
 #include "mxfp4_launch.h"
 

@@ -11,9 +11,11 @@
 // codes and one scale a lane), MFMA i its columns 8i .. 8i+7.
 //
 // What bounds it: the matrix cores and their feeding from LDS where tiles are
-// full (2000 x 14336 x 4096 226 us, 1.04 PFLOP/s, matrix cores 49 % busy; 4096 x
-// 16384 x 14336 1.21 PFLOP/s); with few rows the latency of a step (0.45 us of
-// LDS reads, barrier and 256 matrix-core cycles).  Blocks of 256 weight rows read
+// full (2000 x 14336 x 4096 224 us in a row of calls, 1.05 PFLOP/s; matrix cores
+// 49 % busy over the 241 us of a counted launch; 4096 x 16384 x 14336 1.21
+// PFLOP/s); with few rows the latency of a step (0.45 us of LDS reads, barrier and
+// 256 matrix-core cycles), which nothing hides where there is one block a CU.  A
+// tile's rows are multiplied whether they are there or not.  Blocks of 256 weight rows read
 // X from the caches least often; two or three of them a CU hide each other's
 // barriers (one of 256 x 256: 8192 tokens over 64 experts 1091 us against 1000).
 //
@@ -449,8 +451,9 @@ void launch(LinearArgs a, DType dt, hipStream_t stream) {
 }
 
 // Kernel and K split.
-//   Experts, by rows per expert on average (all rows / experts; 64 experts,
-//   gate-up 3584 x 4096 / down 4096 x 1792, us):
+//   Experts, by rows per expert on average (all rows / experts), as measured for 64
+//   experts and one layer; other counts and sizes follow the same borders (us,
+//   gate-up 3584 x 4096 / down 4096 x 1792):
 //     rows       stream       Low     Medium     Large
 //     0.5       54 / 32   57 / 33    72 / 41
 //     2        117 / 63  101 / 48   111 / 56
