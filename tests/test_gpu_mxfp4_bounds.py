@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 
 import mxfp4_reference as ref
-from test_gpu_moe import check_plan, experts
+from test_gpu_moe import check_grouped, check_plan, experts
 from test_gpu_mxfp4 import HALVES, check_linear, gpu, mx, random_weight, say  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -39,6 +39,35 @@ def test_every_row_is_written_once(mx, dtype, offsets, rows, swiglu):  # noqa: F
         h, bound = ref.swiglu(h, bound)
     ref.check(y, h, bound + ref.rounded(np.abs(h) + bound, dtype), dtype)
     assert (y[:starts[0]] == 0).all() and (y[starts[3]:] == 0).all()
+
+
+# -------------------------------------------------- few experts, many experts
+
+@pytest.mark.parametrize("dtype", HALVES)
+@pytest.mark.parametrize("counts", [[1, 0, 2, 0, 1, 0, 0, 0], [3, 9, 0, 17, 1, 40, 2, 8], [64] * 8])
+def test_few_experts_of_a_long_k(mx, dtype, counts):  # noqa: F811
+    """Eight experts of 14336 columns: less than a row each, ten, and 64."""
+    say("long K %s rows=%d" % (dtype, sum(counts)))
+    rng = np.random.default_rng(sum(counts))
+    codes, scales = experts(rng, 8, 100, 14336, 112, 122)
+    offsets = np.concatenate([[0], np.cumsum(counts)])
+    check_grouped(mx, gpu(rng.standard_normal((offsets[-1], 14336)), dtype), codes, scales, offsets)
+
+
+@pytest.mark.parametrize("E,mean", [(129, 1), (256, 5), (256, 40), (200, 200), (1024, 30)])
+@pytest.mark.parametrize("swiglu", [False, True])
+def test_many_experts_of_every_block_size(mx, E, mean, swiglu):  # noqa: F811
+    """Groups past one and two scans of 64, uneven, for each kernel."""
+    rng = np.random.default_rng([E, mean])
+    counts = rng.integers(0, 2 * mean + 1, E)
+    counts[rng.random(E) < 0.2] = 0
+    counts[E // 2] += max(0, E * mean - counts.sum())     # the mean, by one large expert
+    offsets = np.concatenate([[0], np.cumsum(counts)])
+    say("many experts E=%d rows=%d" % (E, offsets[-1]))
+    codes, scales = experts(rng, E, 40, 64, 112, 122)
+    x = gpu(rng.standard_normal((500, 64)), torch.bfloat16)
+    check_grouped(mx, x, codes, scales, offsets, tokens=rng.integers(-1, 501, offsets[-1]),
+                  swiglu=swiglu)
 
 
 # --------------------------------------------------------------- past 32 bits
