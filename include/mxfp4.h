@@ -30,7 +30,7 @@
  *     a product 0 (inputs without elements may be NULL).
  *   - Row strides count elements, at least K (else W4A16_ERR_INVALID_ARG).
  *   - Alignment: X, its row stride in bytes, codes and the Y of
- *     mxfp4_dequantize 16; other tensors their element size (else
+ *     mxfp4_dequantize 16, dX 16; other tensors their element size (else
  *     W4A16_ERR_MISALIGNED).
  *   - Outputs must not overlap inputs or each other (W4A16_ERR_INVALID_ARG).
  *   - Infinities and NaN are legal in every floating point input.
@@ -161,6 +161,140 @@ int mxfp4_grouped_linear(const void* X, int dtype, int64_t x_rows, int64_t x_str
  * and their own roundings make the error of out 1.4 times as large). */
 int moe_combine(const void* Y, int dtype, int64_t R, int64_t N, const int32_t* positions,
                 const float* weights, int64_t T, int64_t k, void* out, void* stream);
+
+/* ---- Products with an epilogue, and the backward pass of the layers above.
+ * Weights stay what they are (codes): gradients go to activations, biases and
+ * the router. */
+
+/* The activation of an epilogue, z in fp32:
+ *   NONE z;  RELU z where z is not below 0;  SILU z / (1 + exp(-z));
+ *   GELU z erfc(-z / sqrt 2) / 2;
+ *   GELU_TANH z / (1 + exp(-2u)), u = sqrt(2 / pi) (z + 0.044715 z^3), which is
+ *             z (1 + tanh u) / 2;
+ *   SWIGLU of a gate and an up value: gate / (1 + exp(-gate)) * up; N is even,
+ *          columns n < N/2 are gates, n + N/2 their up values.
+ * An infinite z follows the formula (SILU and GELU of -infinity are NaN); its
+ * slope is the limit, 0 or 1. */
+enum {
+    MXFP4_ACT_NONE = 0,
+    MXFP4_ACT_RELU = 1,
+    MXFP4_ACT_SILU = 2,
+    MXFP4_ACT_GELU = 3,
+    MXFP4_ACT_GELU_TANH = 4,
+    MXFP4_ACT_SWIGLU = 5
+};
+
+/* mxfp4_linear with an epilogue, F = N columns of Y (N/2 with SWIGLU):
+ *     z[m,n] = sum_k X[m,k] * W[n,k] + bias[n]
+ *     Y[m,f] = activation(z)[m,f] + residual[m,f]
+ *   bias     in : [N] of X's dtype, or NULL
+ *   residual in : [M, F] of X's dtype, rows r_stride elements apart, or NULL
+ *   Y        out: [M, F] of X's dtype, dense
+ *   Z        out: [M, N] of X's dtype, dense: z, for the backward pass; or NULL
+ * Sums, z and the activation are fp32; Y and Z are rounded once each.
+ * workspace as for mxfp4_linear (mxfp4_linear_workspace_bytes). */
+int mxfp4_linear_act(const void* X, int dtype, int64_t M, int64_t x_stride, const uint8_t* codes,
+                     const uint8_t* scales, int64_t N, int64_t K, const void* bias,
+                     int activation, const void* residual, int64_t r_stride, void* Y, void* Z,
+                     void* workspace, size_t workspace_bytes, void* stream);
+
+/* mxfp4_grouped_linear with the epilogue, each expert with its bias [E, N] (or
+ * NULL).  Y: [R, F]; fp32 with MXFP4_FP32_ROWS (here with SWIGLU too); Z [R, N]
+ * of X's dtype or NULL.  Rows of no expert are 0 in both (no bias). */
+int mxfp4_grouped_linear_act(const void* X, int dtype, int64_t x_rows, int64_t x_stride,
+                             const int32_t* tokens, int64_t R, const uint8_t* codes,
+                             const uint8_t* scales, const int32_t* offsets, int64_t E, int64_t N,
+                             int64_t K, const void* bias, int activation, void* Y, void* Z,
+                             void* stream);
+
+/* Gradient through an activation, and the bias's:
+ *     dZ[r,n] = dY * activation'(Z), with SWIGLU
+ *               dgate = dY * up * silu'(gate), dup = dY * silu(gate)
+ *     dbias[e,n] = sum of dZ[r,n] over the expert's rows, before their rounding
+ *   dY      in : fp16 or bf16 [R, F], rows y_stride elements apart
+ *   Z       in : [R, N] of that dtype, rows z_stride elements apart
+ *   offsets in : int32 [E + 1] as for mxfp4_grouped_linear, or NULL with E = 0:
+ *                one bias, of all rows.  Rows of no expert are in no sum.
+ *   dZ      out: [R, N] of that dtype, dense, every row
+ *   dbias   out: fp32 [E, N] ([1, N] without offsets), or NULL
+ *   workspace  DEVICE, 4-byte aligned, at least
+ *              mxfp4_activation_grad_workspace_bytes(R, N, E) bytes (may be NULL
+ *              where that is 0, or without dbias); no initial contents needed, in
+ *              use until the call's work on the stream has finished.
+ * RELU's slope at 0 is 0.  R = 0 makes dbias 0. */
+size_t mxfp4_activation_grad_workspace_bytes(int64_t R, int64_t N, int64_t E);
+int mxfp4_activation_grad(const void* dY, int dtype, int64_t R, int64_t y_stride, const void* Z,
+                          int64_t z_stride, int64_t N, int activation, const int32_t* offsets,
+                          int64_t E, void* dZ, float* dbias, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/* Gradient through the weight-only product: dX[m,k] = sum_n dY[m,n] * W[n,k].
+ *   dY in : fp16 or bf16 [M, N], rows y_stride elements apart (any N, element
+ *           alignment; rows that start on 16 bytes are read fastest)
+ *   W  in : MXFP4 codes [N, K/2] and scales [N, K/32]
+ *   dX out: [M, K] of dY's dtype, dense, 16-byte aligned
+ * Accuracy as mxfp4_linear, with N terms: |dX - exact| <= (N/8 + 64) 2^-24
+ * sum_n |dY w| + u |exact| + t.  workspace as for mxfp4_linear, with its own size. */
+size_t mxfp4_linear_grad_workspace_bytes(int64_t M, int64_t N, int64_t K);
+int mxfp4_linear_grad(const void* dY, int dtype, int64_t M, int64_t y_stride,
+                      const uint8_t* codes, const uint8_t* scales, int64_t N, int64_t K, void* dX,
+                      void* workspace, size_t workspace_bytes, void* stream);
+
+/* The same by expert: dX[r,k] = sum_n dY[r,n] * W[e][n,k] for offsets[e] <= r <
+ * offsets[e+1] (offsets as for mxfp4_grouped_linear; rows of no expert are 0).
+ * dX: [R, K] of dY's dtype, fp32 with MXFP4_FP32_ROWS added to it; 16-byte
+ * aligned.  The gradient of a gathered input is moe_combine of these rows with
+ * weights of 1. */
+int mxfp4_grouped_linear_grad(const void* dY, int dtype, int64_t R, int64_t y_stride,
+                              const uint8_t* codes, const uint8_t* scales, const int32_t* offsets,
+                              int64_t E, int64_t N, int64_t K, void* dX, void* stream);
+
+/* Balance loss of a routing and the choices of each expert.  P = softmax of a
+ * token's logits over all experts (an expert at -infinity has 0), c_e the ids
+ * equal to e (ids outside [0, E) are no choice), C their sum, T' the tokens with
+ * a logit above -infinity:
+ *     loss = E * sum_e (c_e / C) * (sum_t P[t,e] / T')       (1 when balanced)
+ *   logits in : fp16, bf16 or fp32 [T, E], rows `stride` elements apart
+ *   ids    in : int32 [T, k], 1 <= k <= MOE_MAX_CHOICES
+ *   loss   out: fp32, one value (0 where C or T' is 0)
+ *   counts out: int32 [E + 1]: c_e, and T' in counts[E]
+ *   workspace DEVICE, 4-byte aligned, at least moe_balance_workspace_bytes(T, E, k)
+ *             bytes (may be NULL for T = 0); no initial contents needed, in use
+ *             until the call's work on the stream has finished.
+ * A logit of NaN or +infinity makes the loss NaN.  T k <= 2^29. */
+size_t moe_balance_workspace_bytes(int64_t T, int64_t E, int64_t k);
+int moe_balance(const void* logits, int dtype, int64_t T, int64_t E, int64_t stride,
+                const int32_t* ids, int64_t k, float* loss, int32_t* counts, void* workspace,
+                size_t workspace_bytes, void* stream);
+
+/* Gradient of the routing weights and of the balance loss with respect to the
+ * logits, the choices and counts being constants:
+ *     dlogits[t,e] = sum_j dweights[t,j] * d weights[t,j] / d logits[t,e]
+ *                    + *dloss * d loss / d logits[t,e]
+ *   dweights in : fp32 [T, k], the gradient of moe_route's weights, or NULL (no
+ *                 such part; ids may then be NULL).  renormalize as in moe_route.
+ *                 Choices outside [0, E), or of an expert at -infinity, have none.
+ *   counts   in : int32 [E + 1] of moe_balance (over more tokens than these T
+ *                 where a loss spans several batches), or NULL (no such part)
+ *   dloss    in : fp32, one value, with counts
+ *   dlogits  out: [T, E] of the logits' dtype, dense.  0 for an expert at
+ *                 -infinity.
+ * A row with a NaN or +infinity has NaN gradients. */
+int moe_route_grad(const void* logits, int dtype, int64_t T, int64_t E, int64_t stride,
+                   const int32_t* ids, int64_t k, const float* dweights, int renormalize,
+                   const int32_t* counts, const float* dloss, void* dlogits, void* stream);
+
+/* Gradient of moe_combine: for r = positions[t,j],
+ *     dY[r,n] = weights[t,j] * dout[t,n]
+ *     dweights[t,j] = sum_n dout[t,n] * Y[r,n]     (fp32; 0 for no choice)
+ *   dout   in : fp16 or bf16 [T, N];  Y in: [R, N] of that dtype, or fp32 with
+ *               MXFP4_FP32_ROWS added to the dtype
+ *   tokens in : int32 [R], positions int32 [T, k], of one moe_plan;  weights fp32
+ *   dY     out: [R, N] of dout's dtype; a row that no choice of its token names
+ *               is 0 (choices of one token that name one row add their weights). */
+int moe_combine_grad(const void* dout, int dtype, int64_t T, int64_t N, const void* Y, int64_t R,
+                     const int32_t* tokens, const int32_t* positions, const float* weights,
+                     int64_t k, void* dY, float* dweights, void* stream);
 
 /* Static description of a status code (never NULL). */
 const char* mxfp4_status_string(int status);

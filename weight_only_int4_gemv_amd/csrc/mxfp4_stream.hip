@@ -16,7 +16,7 @@
 // A wave loads a chunk and multiplies it; other waves of the CU cover its wait
 // (holding a second chunk ahead costs as many waves as it gains: 1 x 4096 x
 // 14336 12.3 us against 12.7, 8 x 28672 x 8192 42.3 against 41.1).
-#include "mxfp4_device.h"
+#include "mxfp4_act.h"
 #include "mxfp4_launch.h"
 
 namespace mxfp4 {
@@ -26,7 +26,7 @@ constexpr int kWaves = 8;
 constexpr int kChunkBlocks = 4;  // blocks of a row a wave takes at a time
 constexpr int kTile = 16;
 
-template <typename T, int J>
+template <typename T, int J, bool EPILOGUE>
 __global__ __launch_bounds__(kWaves* kWave) void stream_kernel(LinearArgs a) {
     constexpr bool kIsF16 = __is_same(T, F16);
     const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
@@ -187,6 +187,11 @@ __global__ __launch_bounds__(kWaves* kWave) void stream_kernel(LinearArgs a) {
             h[0] += part[v][j0][r][n % kTile];
             if (J > 1 && a.swiglu) h[1] += part[v][j0 + J / 2][r][n % kTile];
         }
+        if constexpr (EPILOGUE) {
+            const float z[1] = {h[0]}, up[1] = {h[1]};
+            finish_columns<T, 1>(a, t.expert, t.row0 + r, col0 + n, z, up);
+            continue;
+        }
         const float y = a.swiglu ? silu(h[0]) * h[1] : h[0];
         const int64_t at = (int64_t)(t.row0 + r) * F + col0 + n;
         if (a.part != nullptr) a.part[at] = y;
@@ -199,8 +204,11 @@ hipError_t launch(const LinearArgs& a, DType dt, hipStream_t stream) {
     const int F = a.swiglu ? a.N / 2 : a.N, per = a.swiglu ? J * kTile / 2 : J * kTile;
     const int64_t slots = a.offsets ? tile_slots(a.R, a.E, kTile) : (a.R + kTile - 1) / kTile;
     const dim3 grid = slot_grid((F + per - 1) / per, slots);
-    if (dt == kF16) stream_kernel<F16, J><<<grid, kWaves * kWave, 0, stream>>>(a);
-    else stream_kernel<BF16, J><<<grid, kWaves * kWave, 0, stream>>>(a);
+    constexpr int kThreads = kWaves * kWave;
+    if (a.epilogue && dt == kF16) stream_kernel<F16, J, true><<<grid, kThreads, 0, stream>>>(a);
+    else if (a.epilogue) stream_kernel<BF16, J, true><<<grid, kThreads, 0, stream>>>(a);
+    else if (dt == kF16) stream_kernel<F16, J, false><<<grid, kThreads, 0, stream>>>(a);
+    else stream_kernel<BF16, J, false><<<grid, kThreads, 0, stream>>>(a);
     return hipGetLastError();
 }
 

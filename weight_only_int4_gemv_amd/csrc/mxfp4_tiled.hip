@@ -21,6 +21,7 @@
 //
 // With SwiGLU a block's weight rows are 32 gate rows, their 32 up rows, the
 // next 32 gate rows ..., so that a wave holds both factors of its outputs.
+#include "mxfp4_act.h"
 #include "mxfp4_launch.h"
 #include "mxfp4_tile.h"
 
@@ -65,7 +66,7 @@ struct Tiling {
 __device__ __forceinline__ int x_swizzle(int r) { return (r >> 1) & 7; }
 __device__ __forceinline__ int w_swizzle(int r) { return (r >> 3) & 1; }
 
-template <typename T, class C>
+template <typename T, class C, bool EPILOGUE>
 __global__ __launch_bounds__(C::kThreads, C::kPerCu * C::kWaves / 4) void tiled_kernel(LinearArgs a) {
     constexpr bool kIsF16 = __is_same(T, F16);
     constexpr int MT = C::MT, NT = C::NT;
@@ -376,15 +377,16 @@ __global__ __launch_bounds__(C::kThreads, C::kPerCu * C::kWaves / 4) void tiled_
     for (int m = 0; m < MT; ++m) {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            if (NT > 1 && a.swiglu && (n & 1)) continue;
-            const int at = r31 * C::kPitch + (a.swiglu ? n / 2 : n) * 32 + 4 * half;
+            if (!EPILOGUE && NT > 1 && a.swiglu && (n & 1)) continue;
+            const int at = r31 * C::kPitch + (!EPILOGUE && a.swiglu ? n / 2 : n) * 32 + 4 * half;
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
                 float4_t v;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     v[i] = acc[m][n][4 * g + i];
-                    if (NT > 1 && a.swiglu) v[i] = silu(v[i]) * acc[m][n | 1][4 * g + i];
+                    if (!EPILOGUE && NT > 1 && a.swiglu)
+                        v[i] = silu(v[i]) * acc[m][n | 1][4 * g + i];
                 }
                 *(float4_t*)&turn[at + 8 * g] = v;
             }
@@ -393,7 +395,27 @@ __global__ __launch_bounds__(C::kThreads, C::kPerCu * C::kWaves / 4) void tiled_
         __builtin_amdgcn_wave_barrier();
         const int rows = min(32, t.rows - 32 * m);
         const int64_t out0 = (int64_t)(t.row0 + 32 * m) * F + wcol0;
-        if (a.part != nullptr) {
+        if constexpr (EPILOGUE) {
+            auto finish = [&](auto vec) {
+                constexpr int VEC = decltype(vec)::value;
+                const int chunks = wcols / VEC;
+#pragma unroll 1
+                for (int i = lane; i < 32 * chunks; i += kWave) {
+                    const int r = i / chunks, c = i % chunks * VEC;
+                    if (r >= rows || c >= cols) continue;
+                    const float* from = &turn[r * C::kPitch + c];
+                    float h[VEC], up[VEC] = {};
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) {
+                        h[j] = from[j];
+                        if (NT > 1 && a.swiglu) up[j] = from[32 + j];
+                    }
+                    finish_columns<T, VEC>(a, t.expert, t.row0 + 32 * m + r, wcol0 + c, h, up);
+                }
+            };
+            if (finish_wide(a)) finish(Int<8>());
+            else finish(Int<1>());
+        } else if (a.part != nullptr) {
             float* p = a.part + (int64_t)slice * a.R * F + out0;
             if (F % 4 == 0 && (uintptr_t)a.part % 16 == 0) {
                 for (int i = lane; i < 32 * C::WN / 4; i += kWave) {
@@ -443,10 +465,14 @@ void launch(LinearArgs a, DType dt, hipStream_t stream) {
     const int64_t blocks = slots * a.nt * a.slices;
     for (a.first = 0; a.first < blocks; a.first += kMaxGrid) {
         const unsigned grid = (unsigned)(blocks - a.first < kMaxGrid ? blocks - a.first : kMaxGrid);
-        if (dt == kF16)
-            tiled_kernel<F16, C><<<grid, C::kThreads, 0, stream>>>(a);
+        if (a.epilogue && dt == kF16)
+            tiled_kernel<F16, C, true><<<grid, C::kThreads, 0, stream>>>(a);
+        else if (a.epilogue)
+            tiled_kernel<BF16, C, true><<<grid, C::kThreads, 0, stream>>>(a);
+        else if (dt == kF16)
+            tiled_kernel<F16, C, false><<<grid, C::kThreads, 0, stream>>>(a);
         else
-            tiled_kernel<BF16, C><<<grid, C::kThreads, 0, stream>>>(a);
+            tiled_kernel<BF16, C, false><<<grid, C::kThreads, 0, stream>>>(a);
     }
 }
 
@@ -518,6 +544,30 @@ hipError_t launch_linear(LinearArgs a, DType dt, float* part, hipStream_t stream
     }
     if (c.slices > 1) launch_add_slices(a.part, a.slices, (int64_t)a.R * a.N, a.Y, dt, stream);
     return hipGetLastError();
+}
+
+// Unsplit, the product's own kernel ends with the epilogue; K slices leave their sums to a
+// second launch, which has to read them anyway.
+hipError_t launch_linear_act(LinearArgs a, DType dt, float* part, hipStream_t stream) {
+    Choice c = choose(a.R, a.E, a.N, a.K, a.offsets != nullptr, part != nullptr);
+    a.slices = c.slices, a.steps = c.steps;
+    if (c.slices > 1) {
+        a.part = part;
+    } else {
+        a.epilogue = true;
+        a.swiglu = a.act == kSwiglu;
+        // A wave of Narrow has no place for a gate and its up rows.
+        if (a.swiglu && c.kernel == kNarrow) c.kernel = kMedium;
+    }
+    switch (c.kernel) {
+        case kStream: return launch_stream(a, dt, stream);
+        case kLow: launch<Low>(a, dt, stream); break;
+        case kNarrow: launch<Narrow>(a, dt, stream); break;
+        case kMedium: launch<Medium>(a, dt, stream); break;
+        case kLarge: launch<Large>(a, dt, stream); break;
+    }
+    const hipError_t e = hipGetLastError();
+    return e == hipSuccess && c.slices > 1 ? launch_finish(a, dt, stream) : e;
 }
 
 }  // namespace mxfp4

@@ -15,6 +15,23 @@ a missing library or a non-gfx950 device is an error.
     H = grouped_linear(X, c1, s1, p.offsets, tokens=p.tokens, swiglu=True)
     H = grouped_linear(H, c2, s2, p.offsets, dtype=torch.float32)
     out = combine(H, p.positions, weights, dtype=X.dtype)       # [T, N]
+
+Products with an epilogue, and the backward pass (weights stay codes: gradients go to
+activations, biases and the router):
+
+    Y, Z = linear_act(X, codes, scales, bias, activation="gelu", residual=R, save=True)
+    dZ, dbias = activation_grad(dY, Z, "gelu")
+    dX = linear_grad(dZ, codes, scales)
+
+    H, Z = grouped_linear_act(X, c1, s1, p.offsets, tokens=p.tokens, bias=b1,
+                              activation="swiglu", save=True)
+    rows, dweights = combine_grad(dout, Y, p.tokens, p.positions, weights)
+    dH = grouped_linear_grad(rows, c2, s2, p.offsets)
+    dZ, db1 = activation_grad(dH, Z, "swiglu", offsets=p.offsets)
+    dX = grouped_linear_grad(dZ, c1, s1, p.offsets, dtype=torch.float32)
+    dx = combine(dX, p.positions, torch.ones_like(weights), dtype=X.dtype)
+    loss, counts = balance(logits, ids)
+    dlogits = route_grad(logits, ids, dweights, counts=counts, dloss=dloss)
 """
 from __future__ import annotations
 
@@ -33,6 +50,9 @@ MAX_CHOICES = 32
 _FLOATS = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
 _HALVES = {torch.float16: 0, torch.bfloat16: 1}
 _FP32_ROWS = 16                  # added to a dtype: the experts' rows are fp32
+ACTIVATIONS = ("none", "relu", "silu", "gelu", "gelu_tanh", "swiglu")
+_ACT = {name: i for i, name in enumerate(ACTIVATIONS)}
+_SWIGLU = _ACT["swiglu"]
 
 _p = ctypes.c_void_p
 _i64 = ctypes.c_int64
@@ -48,9 +68,21 @@ _SIGNATURES = {
     "moe_route": [_p, _int, _i64, _i64, _i64, _i64, _int, _p, _p, _p],
     "moe_plan": [_p, _i64, _i64, _i64, _p, _p, _p, _p, _size, _p],
     "moe_combine": [_p, _int, _i64, _i64, _p, _p, _i64, _i64, _p, _p],
+    "mxfp4_linear_act": [_p, _int, _i64, _i64, _p, _p, _i64, _i64, _p, _int, _p, _i64, _p, _p, _p,
+                         _size, _p],
+    "mxfp4_grouped_linear_act": [_p, _int, _i64, _i64, _p, _i64, _p, _p, _p, _i64, _i64, _i64, _p,
+                                 _int, _p, _p, _p],
+    "mxfp4_activation_grad": [_p, _int, _i64, _i64, _p, _i64, _i64, _int, _p, _i64, _p, _p, _p,
+                              _size, _p],
+    "mxfp4_linear_grad": [_p, _int, _i64, _i64, _p, _p, _i64, _i64, _p, _p, _size, _p],
+    "mxfp4_grouped_linear_grad": [_p, _int, _i64, _i64, _p, _p, _p, _i64, _i64, _i64, _p, _p],
+    "moe_balance": [_p, _int, _i64, _i64, _i64, _p, _i64, _p, _p, _p, _size, _p],
+    "moe_route_grad": [_p, _int, _i64, _i64, _i64, _p, _i64, _p, _int, _p, _p, _p, _p],
+    "moe_combine_grad": [_p, _int, _i64, _i64, _p, _i64, _p, _p, _p, _i64, _p, _p, _p],
 }
 _SIZES = ("mxfp4_linear_workspace_bytes", "mxfp4_matmul_workspace_bytes",
-          "moe_plan_workspace_bytes")
+          "moe_plan_workspace_bytes", "mxfp4_activation_grad_workspace_bytes",
+          "mxfp4_linear_grad_workspace_bytes", "moe_balance_workspace_bytes")
 _lib = None
 
 
@@ -128,7 +160,7 @@ def _stream(*tensors) -> int:
 def _row_stride(t: torch.Tensor, name: str) -> int:
     """Elements between the rows of a 2-d tensor whose rows are dense."""
     rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
+    if rows and cols > 1 and t.stride(1) != 1:
         raise ValueError("the rows of %s must be dense, got strides %s" % (name, t.stride()))
     if rows <= 1 or cols == 0:
         return cols
@@ -399,3 +431,320 @@ def combine(Y: torch.Tensor, positions: torch.Tensor, weights: torch.Tensor,
                            positions.data_ptr(), weights.data_ptr(), T, k, out.data_ptr(),
                            _stream(Y, positions, weights, out)))
     return out
+
+
+# ------------------------------------------- products with an epilogue, gradients
+
+def _activation(name, N: int) -> int:
+    act = _ACT.get("none" if name is None else name)
+    if act is None:
+        raise ValueError("activation must be one of %s, got %r" % (", ".join(ACTIVATIONS), name))
+    if act == _SWIGLU and N % 2:
+        raise ValueError("swiglu takes an even number of gate and up columns, got %d" % N)
+    return act
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _given(*tensors):
+    return tuple(t for t in tensors if t is not None)
+
+
+def _bias(bias, shape, X: torch.Tensor) -> None:
+    if bias is None:
+        return
+    _need(bias, "bias", (X.dtype,), len(shape))
+    if tuple(bias.shape) != shape:
+        raise ValueError("bias has shape %s, want %s" % (tuple(bias.shape), shape))
+
+
+def linear_act(X: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
+               bias: torch.Tensor = None, activation: str = None, residual: torch.Tensor = None,
+               save: bool = False, Y: torch.Tensor = None, Z: torch.Tensor = None,
+               workspace: torch.Tensor = None):
+    """Y = activation(X W^T + bias) + residual: X fp16 or bf16 [M, K] (rows as in
+    linear()), MXFP4 weights [N, K], bias [N] and residual [M, F] (dense rows) of X's
+    dtype or None.  activation: one of ACTIVATIONS; swiglu takes weights of gate rows,
+    then up rows, F = N / 2, otherwise F = N.  Y [M, F] is of X's dtype; with save (or
+    Z given) the result is (Y, Z), Z [M, N] what the activation was applied to.
+    workspace as in linear()."""
+    lib = library()
+    N, K = _weights(codes, scales, 2)
+    _need(X, "X", _HALVES, 2, dense=False)
+    M = X.shape[0]
+    if X.shape[1] != K:
+        raise ValueError("X has %d columns, K = %d" % (X.shape[1], K))
+    act = _activation(activation, N)
+    F = N // 2 if act == _SWIGLU else N
+    stride = _row_stride(X, "X")
+    _bias(bias, (N,), X)
+    r_stride = F
+    if residual is not None:
+        _need(residual, "residual", (X.dtype,), 2, dense=False)
+        if tuple(residual.shape) != (M, F):
+            raise ValueError("residual has shape %s, want %s" % (tuple(residual.shape), (M, F)))
+        r_stride = _row_stride(residual, "residual")
+    Y = _out(Y, (M, F), X.dtype, X, "Y")
+    save = save or Z is not None
+    if save:
+        Z = _out(Z, (M, N), X.dtype, X, "Z")
+    ws, ws_bytes, keep = _workspace(_workspace_bytes("mxfp4_linear_workspace_bytes", M, N, K),
+                                    workspace, X)
+    _check("mxfp4_linear_act",
+           lib.mxfp4_linear_act(X.data_ptr(), _HALVES[X.dtype], M, stride, codes.data_ptr(),
+                                scales.data_ptr(), N, K, _ptr(bias), act, _ptr(residual), r_stride,
+                                Y.data_ptr(), _ptr(Z), ws, ws_bytes,
+                                _stream(X, codes, scales, Y, *_given(bias, residual, Z), *keep)))
+    return (Y, Z) if save else Y
+
+
+def grouped_linear_act(X: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
+                       offsets: torch.Tensor, tokens: torch.Tensor = None,
+                       bias: torch.Tensor = None, activation: str = None, save: bool = False,
+                       Y: torch.Tensor = None, Z: torch.Tensor = None,
+                       dtype: torch.dtype = None):
+    """grouped_linear() with the epilogue of linear_act() (no residual), each expert
+    with its bias, [E, N] of X's dtype or None.  Y [R, F] of dtype: X's (the default)
+    or fp32; with save (or Z given) the result is (Y, Z), Z [R, N] of X's dtype.  Rows
+    of no expert are 0 in both."""
+    lib = library()
+    E, N, K = _weights(codes, scales, 3)
+    _need(X, "X", _HALVES, 2, dense=False)
+    if X.shape[1] != K:
+        raise ValueError("X has %d columns, K = %d" % (X.shape[1], K))
+    if not 1 <= E <= MAX_EXPERTS:
+        raise ValueError("codes hold %d experts, want 1 to %d" % (E, MAX_EXPERTS))
+    act = _activation(activation, N)
+    F = N // 2 if act == _SWIGLU else N
+    if dtype not in (None, X.dtype, torch.float32):
+        raise ValueError("dtype must be %s or torch.float32, got %s" % (X.dtype, dtype))
+    rows32 = dtype == torch.float32
+    _need(offsets, "offsets", _I32, 1)
+    if offsets.shape[0] != E + 1:
+        raise ValueError("offsets has %d entries, want %d" % (offsets.shape[0], E + 1))
+    R = X.shape[0]
+    if tokens is not None:
+        _need(tokens, "tokens", _I32, 1)
+        R = tokens.shape[0]
+    stride = _row_stride(X, "X")
+    _bias(bias, (E, N), X)
+    Y = _out(Y, (R, F), dtype or X.dtype, X, "Y")
+    save = save or Z is not None
+    if save:
+        Z = _out(Z, (R, N), X.dtype, X, "Z")
+    _check("mxfp4_grouped_linear_act",
+           lib.mxfp4_grouped_linear_act(X.data_ptr(),
+                                        _HALVES[X.dtype] + (_FP32_ROWS if rows32 else 0),
+                                        X.shape[0], stride, _ptr(tokens), R, codes.data_ptr(),
+                                        scales.data_ptr(), offsets.data_ptr(), E, N, K,
+                                        _ptr(bias), act, Y.data_ptr(), _ptr(Z),
+                                        _stream(X, codes, scales, offsets, Y,
+                                                *_given(tokens, bias, Z))))
+    return (Y, Z) if save else Y
+
+
+def activation_grad(dY: torch.Tensor, Z: torch.Tensor, activation: str,
+                    offsets: torch.Tensor = None, bias: bool = True, dZ: torch.Tensor = None,
+                    dbias: torch.Tensor = None, workspace: torch.Tensor = None):
+    """dZ = dY * activation'(Z) and the bias's gradient, the sum of dZ's rows before
+    their rounding: dY fp16 or bf16 [R, F] and Z [R, N] of that dtype (dense rows; F =
+    N / 2 with swiglu) -> (dZ [R, N], dbias fp32 [N], with offsets int32 [E + 1] by
+    expert, [E, N]); without bias dZ alone.  workspace: uint8 of
+    mxfp4_activation_grad_workspace_bytes, else allocated per call where used."""
+    lib = library()
+    _need(dY, "dY", _HALVES, 2, dense=False)
+    _need(Z, "Z", (dY.dtype,), 2, dense=False)
+    R, N = Z.shape
+    act = _activation(activation, N)
+    F = N // 2 if act == _SWIGLU else N
+    if tuple(dY.shape) != (R, F):
+        raise ValueError("dY has shape %s, want %s" % (tuple(dY.shape), (R, F)))
+    y_stride, z_stride = _row_stride(dY, "dY"), _row_stride(Z, "Z")
+    E, shape = 0, (N,)
+    if offsets is not None:
+        _need(offsets, "offsets", _I32, 1)
+        E = offsets.shape[0] - 1
+        if not 1 <= E <= MAX_EXPERTS:
+            raise ValueError("offsets are of %d experts, want 1 to %d" % (E, MAX_EXPERTS))
+        shape = (E, N)
+    dZ = _out(dZ, (R, N), dY.dtype, dY, "dZ")
+    bias = bias or dbias is not None
+    ws, ws_bytes, keep = None, 0, ()
+    if bias:
+        dbias = _out(dbias, shape, torch.float32, dY, "dbias")
+        ws, ws_bytes, keep = _workspace(
+            _workspace_bytes("mxfp4_activation_grad_workspace_bytes", R, N, E), workspace, dY)
+    _check("mxfp4_activation_grad",
+           lib.mxfp4_activation_grad(dY.data_ptr(), _HALVES[dY.dtype], R, y_stride, Z.data_ptr(),
+                                     z_stride, N, act, _ptr(offsets), E, dZ.data_ptr(),
+                                     _ptr(dbias), ws, ws_bytes,
+                                     _stream(dY, Z, dZ, *_given(offsets, dbias), *keep)))
+    return (dZ, dbias) if bias else dZ
+
+
+def linear_grad_workspace(M: int, N: int, K: int, device="cuda") -> torch.Tensor:
+    """A workspace for linear_grad() (uint8, at least 1 byte)."""
+    n = _workspace_bytes("mxfp4_linear_grad_workspace_bytes", M, N, K)
+    return torch.empty(max(1, n), dtype=torch.uint8, device=device)
+
+
+def linear_grad(dY: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
+                dX: torch.Tensor = None, workspace: torch.Tensor = None) -> torch.Tensor:
+    """The gradient of linear() with respect to X: dY fp16 or bf16 [M, N] (dense rows)
+    times MXFP4 weights [N, K] -> dX [M, K] of dY's dtype, on 16 bytes.  Rows of dY that
+    start on 16 bytes are read fastest.  workspace: from linear_grad_workspace(), else
+    allocated per call where the shape uses one."""
+    lib = library()
+    N, K = _weights(codes, scales, 2)
+    _need(dY, "dY", _HALVES, 2, dense=False)
+    M = dY.shape[0]
+    if dY.shape[1] != N:
+        raise ValueError("dY has %d columns, N = %d" % (dY.shape[1], N))
+    stride = _row_stride(dY, "dY")
+    dX = _out(dX, (M, K), dY.dtype, dY, "dX")
+    ws, ws_bytes, keep = _workspace(_workspace_bytes("mxfp4_linear_grad_workspace_bytes", M, N, K),
+                                    workspace, dY)
+    _check("mxfp4_linear_grad",
+           lib.mxfp4_linear_grad(dY.data_ptr(), _HALVES[dY.dtype], M, stride, codes.data_ptr(),
+                                 scales.data_ptr(), N, K, dX.data_ptr(), ws, ws_bytes,
+                                 _stream(dY, codes, scales, dX, *keep)))
+    return dX
+
+
+def grouped_linear_grad(dY: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
+                        offsets: torch.Tensor, dX: torch.Tensor = None,
+                        dtype: torch.dtype = None) -> torch.Tensor:
+    """The gradient of grouped_linear()'s product with respect to its rows: row r of dX
+    = row r of dY (fp16 or bf16 [R, N]) times the MXFP4 weights [E, N, K] of its expert;
+    rows of no expert are 0.  dX [R, K] of dtype: dY's (the default) or fp32, for
+    combine() with weights of 1, which gives the gradient of a gathered X."""
+    lib = library()
+    E, N, K = _weights(codes, scales, 3)
+    _need(dY, "dY", _HALVES, 2, dense=False)
+    R = dY.shape[0]
+    if dY.shape[1] != N:
+        raise ValueError("dY has %d columns, N = %d" % (dY.shape[1], N))
+    if not 1 <= E <= MAX_EXPERTS:
+        raise ValueError("codes hold %d experts, want 1 to %d" % (E, MAX_EXPERTS))
+    if dtype not in (None, dY.dtype, torch.float32):
+        raise ValueError("dtype must be %s or torch.float32, got %s" % (dY.dtype, dtype))
+    rows32 = dtype == torch.float32
+    _need(offsets, "offsets", _I32, 1)
+    if offsets.shape[0] != E + 1:
+        raise ValueError("offsets has %d entries, want %d" % (offsets.shape[0], E + 1))
+    stride = _row_stride(dY, "dY")
+    dX = _out(dX, (R, K), dtype or dY.dtype, dY, "dX")
+    _check("mxfp4_grouped_linear_grad",
+           lib.mxfp4_grouped_linear_grad(dY.data_ptr(),
+                                         _HALVES[dY.dtype] + (_FP32_ROWS if rows32 else 0), R,
+                                         stride, codes.data_ptr(), scales.data_ptr(),
+                                         offsets.data_ptr(), E, N, K, dX.data_ptr(),
+                                         _stream(dY, codes, scales, offsets, dX)))
+    return dX
+
+
+def _router(logits: torch.Tensor, ids):
+    """(T, E, k, row stride) of logits [T, E] and ids [T, k] (None: k = 1)."""
+    _need(logits, "logits", _FLOATS, 2, dense=False)
+    T, E = logits.shape
+    if not 1 <= E <= MAX_EXPERTS:
+        raise ValueError("logits have %d experts, want 1 to %d" % (E, MAX_EXPERTS))
+    k = 1
+    if ids is not None:
+        _need(ids, "ids", _I32, 2)
+        k = ids.shape[1]
+        if ids.shape[0] != T or not 1 <= k <= MAX_CHOICES:
+            raise ValueError("ids have shape %s, want (%d, 1 to %d)"
+                             % (tuple(ids.shape), T, MAX_CHOICES))
+    return T, E, k, _row_stride(logits, "logits")
+
+
+def balance(logits: torch.Tensor, ids: torch.Tensor, loss: torch.Tensor = None,
+            counts: torch.Tensor = None, workspace: torch.Tensor = None):
+    """The balance loss E sum_e (c_e / C) (mean of softmax(logits)[:, e]) of a routing:
+    logits [T, E] (fp16, bf16 or fp32, dense rows), ids int32 [T, k] -> (loss fp32 [],
+    counts int32 [E + 1]): counts[e] = c_e the choices of expert e, C their sum,
+    counts[E] the tokens with a usable expert, over which the mean is taken.
+    workspace: uint8 of moe_balance_workspace_bytes, else allocated per call."""
+    lib = library()
+    _need(ids, "ids", _I32, 2)
+    T, E, k, stride = _router(logits, ids)
+    loss = _out(loss, (), torch.float32, logits, "loss")
+    counts = _out(counts, (E + 1,), torch.int32, logits, "counts")
+    ws, ws_bytes, keep = _workspace(_workspace_bytes("moe_balance_workspace_bytes", T, E, k),
+                                    workspace, logits)
+    _check("moe_balance",
+           lib.moe_balance(logits.data_ptr(), _FLOATS[logits.dtype], T, E, stride, ids.data_ptr(),
+                           k, loss.data_ptr(), counts.data_ptr(), ws, ws_bytes,
+                           _stream(logits, ids, loss, counts, *keep)))
+    return loss, counts
+
+
+def route_grad(logits: torch.Tensor, ids: torch.Tensor = None, dweights: torch.Tensor = None,
+               renormalize: bool = True, counts: torch.Tensor = None, dloss: torch.Tensor = None,
+               dlogits: torch.Tensor = None) -> torch.Tensor:
+    """dlogits [T, E] of the logits' dtype: the gradient of route()'s weights for ids
+    int32 [T, k] and dweights fp32 [T, k] (None: no such part), plus dloss (fp32, one
+    value) times the gradient of balance()'s loss for its counts (None: no such part).
+    The choices and the counts are constants."""
+    lib = library()
+    T, E, k, stride = _router(logits, ids)
+    if dweights is None and counts is None:
+        raise ValueError("dweights or counts must be given")
+    if dweights is not None:
+        if ids is None:
+            raise ValueError("dweights need ids")
+        _need(dweights, "dweights", _F32, 2)
+        if dweights.shape != ids.shape:
+            raise ValueError("dweights shape %s, ids %s"
+                             % (tuple(dweights.shape), tuple(ids.shape)))
+    if (counts is None) != (dloss is None):
+        raise ValueError("counts and dloss go together")
+    if counts is not None:
+        _need(counts, "counts", _I32, 1)
+        _need(dloss, "dloss", _F32, 0)
+        if counts.shape[0] != E + 1 or dloss.numel() != 1:
+            raise ValueError("counts have %d entries, want %d; dloss %d, want 1"
+                             % (counts.shape[0], E + 1, dloss.numel()))
+    dlogits = _out(dlogits, (T, E), logits.dtype, logits, "dlogits")
+    _check("moe_route_grad",
+           lib.moe_route_grad(logits.data_ptr(), _FLOATS[logits.dtype], T, E, stride, _ptr(ids), k,
+                              _ptr(dweights), 1 if renormalize else 0, _ptr(counts), _ptr(dloss),
+                              dlogits.data_ptr(),
+                              _stream(logits, dlogits, *_given(ids, dweights, counts, dloss))))
+    return dlogits
+
+
+def combine_grad(dout: torch.Tensor, Y: torch.Tensor, tokens: torch.Tensor,
+                 positions: torch.Tensor, weights: torch.Tensor, dY: torch.Tensor = None,
+                 dweights: torch.Tensor = None):
+    """The gradient of combine(): dout fp16 or bf16 [T, N], Y [R, N] of that dtype or
+    fp32, tokens and positions of the plan, weights fp32 [T, k] -> (dY [R, N] of dout's
+    dtype, 0 in rows of no choice; dweights fp32 [T, k], 0 for no choice)."""
+    lib = library()
+    _need(dout, "dout", _HALVES, 2)
+    _need(Y, "Y", (dout.dtype, torch.float32), 2)
+    _need(tokens, "tokens", _I32, 1)
+    _need(positions, "positions", _I32, 2)
+    _need(weights, "weights", _F32, 2)
+    T, N = dout.shape
+    R, k = Y.shape[0], positions.shape[1]
+    if Y.shape[1] != N or tokens.shape[0] != R:
+        raise ValueError("Y has shape %s, want (%d tokens of the plan, %d)"
+                         % (tuple(Y.shape), tokens.shape[0], N))
+    if positions.shape != weights.shape or positions.shape[0] != T:
+        raise ValueError("positions shape %s, weights %s, want (%d, k)"
+                         % (tuple(positions.shape), tuple(weights.shape), T))
+    if not 1 <= k <= MAX_CHOICES:
+        raise ValueError("positions have %d choices a token, want 1 to %d" % (k, MAX_CHOICES))
+    dY = _out(dY, (R, N), dout.dtype, dout, "dY")
+    dweights = _out(dweights, (T, k), torch.float32, dout, "dweights")
+    rows32 = Y.dtype == torch.float32
+    _check("moe_combine_grad",
+           lib.moe_combine_grad(dout.data_ptr(), _HALVES[dout.dtype] + (_FP32_ROWS if rows32 else 0),
+                                T, N, Y.data_ptr(), R, tokens.data_ptr(), positions.data_ptr(),
+                                weights.data_ptr(), k, dY.data_ptr(), dweights.data_ptr(),
+                                _stream(dout, Y, tokens, positions, weights, dY, dweights)))
+    return dY, dweights
