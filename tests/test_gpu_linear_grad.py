@@ -35,6 +35,52 @@ def test_linear_grad(mx, dtype, M, N, K):  # noqa: F811
     check_grad(mx, gpu(rng.standard_normal((M, N)), dtype), codes, scales)
 
 
+# Rows that fill the chip once with blocks of 128, 96, 64 and 32 rows.
+TILES = [65500, 49100, 32700, 16300]
+
+
+@pytest.mark.parametrize("dtype", HALVES)
+@pytest.mark.parametrize("M", TILES)
+@pytest.mark.parametrize("N,K", [(392, 256), (331, 224), (200, 160)])
+def test_every_tiling(mx, dtype, M, N, K):  # noqa: F811
+    """Several steps of each; rows of dY on 16 bytes and not, scales on words and not, ends of the
+    rows, the weight rows and the columns inside a tile."""
+    say("linear_grad tilings %s M=%d N=%d K=%d" % (dtype, M, N, K))
+    rng = np.random.default_rng([M, N])
+    codes, scales = weights(rng, (N, K))
+    check_grad(mx, gpu(rng.standard_normal((M, N)), dtype), codes, scales)
+
+
+@pytest.mark.parametrize("dtype", HALVES)
+@pytest.mark.parametrize("M", TILES)
+@pytest.mark.parametrize("low,high", [(90, 120), (118, 150), (0, 3)])
+def test_every_tiling_scale_ranges(mx, dtype, M, low, high):  # noqa: F811
+    say("linear_grad tilings scales %s M=%d %d..%d" % (dtype, M, low, high))
+    rng = np.random.default_rng([M, low])
+    N, K = 264, 128
+    codes, scales = weights(rng, (N, K), 118, 126)
+    scales[150:] = weights(rng, (N - 150, K), low, high)[1]      # from the third step on
+    dy = gpu(rng.standard_normal((M, N)) * 2.0 ** -6, dtype)
+    check_grad(mx, dy, codes, scales)
+    scales[190, 1], scales[7, 3] = 254, 253
+    check_grad(mx, dy, codes, scales)
+    scales[263, 2] = 255
+    assert mx.linear_grad(dy, gpu(codes), gpu(scales))[:, 64:96].isnan().all()
+
+
+@pytest.mark.parametrize("M", [4, 50, 300])
+def test_scales_at_any_byte(mx, M):  # noqa: F811
+    rng = np.random.default_rng(M)
+    codes, scales = weights(rng, (520, 512))
+    room = torch.empty(scales.size + 3, dtype=torch.uint8, device="cuda")
+    dy = gpu(rng.standard_normal((M, 520)), torch.bfloat16)
+    want = mx.linear_grad(dy, gpu(codes), gpu(scales))
+    for at in (1, 2, 3):
+        view = room[at:at + scales.size].view(scales.shape)
+        view.copy_(gpu(scales))
+        assert torch.equal(mx.linear_grad(dy, gpu(codes), view), want)
+
+
 @pytest.mark.parametrize("dtype", HALVES)
 @pytest.mark.parametrize("M", [3, 40, 200])
 def test_strides_and_alignment(mx, dtype, M):  # noqa: F811

@@ -48,6 +48,20 @@ struct Int {
     static constexpr int value = N;
 };
 
+// f(Int<FROM>()) ... f(Int<TO - 1>()).
+template <int FROM, int TO, class F>
+__device__ __forceinline__ void units(F f) {
+    if constexpr (FROM < TO) {
+        f(Int<FROM>());
+        units<FROM + 1, TO>(f);
+    }
+}
+
+template <class F, int N>
+__device__ __forceinline__ void each_of(F f, Int<N>) {
+    units<0, N>(f);
+}
+
 // The lane's eight weight rows n0 .. n0 + 7 of one row of dY; rows past N count 0.
 __device__ __forceinline__ uint4_t load_dy(const uint16_t* row, int n0, int N, bool wide) {
     uint4_t v = {0, 0, 0, 0};
@@ -223,46 +237,48 @@ __global__ __launch_bounds__(kWaves* kWave) void stream_grad_kernel(GradArgs a) 
 
 // ------------------------------------------------------------------- tiled
 //
-// Many rows.  A block of WM x WK waves owns 16 MT WM rows of dY and 128 WK columns of dX; N is
-// walked in steps of 64 weight rows, whose dY tile and codes go from global memory straight to
-// LDS, STAGES steps deep.  Scales come through registers, as fp32: they follow the rows.
+// Many rows.  A block of four waves owns 16 MT rows of dY and 256 columns of dX, each wave all
+// rows and 64 columns, so that a weight is converted once per block: a vector instruction per
+// weight pair is what bounds the product (two of them fit beside a 16x16x32 matrix instruction,
+// a third costs a quarter of the rate).  N is walked in steps of 64 weight rows, whose dY tile
+// and codes go from global memory straight to LDS, kStages steps deep.  The scales' bytes go there
+// a step earlier and become fp32 in LDS a step before their use.  (Loaded to registers they cost
+// the copies their depth: the wait for them is a wait for every copy on its way.)
 //
-// In LDS, 16-byte chunk c of row m of dY stands at c ^ x_swizzle(m), so that 16 lanes that read
-// one chunk of 16 rows meet all banks once; of each 32 weight rows those that lane groups 0 to 3
-// read together (8 g + i for one i) stand side by side, 64 bytes of a wave's 128 columns each.
+// In LDS, 16-byte chunk c of row m of dY stands at c ^ x_swizzle(m): 16 lanes that read one chunk
+// of 16 rows meet all banks once.  Of each 32 weight rows, row 8 g + i has place 4 i + g (lane
+// groups g = 0 .. 3 read one i together) and chunk c of it stands at c ^ w_swizzle(g).
 constexpr int kStep = 64;
 constexpr int kXRow = kStep * 2;                            // bytes of a row of the dY tile
-constexpr int kWaveCols = 128;
-constexpr int kSubBytes = kStepRows * kWaveCols / 2;        // 32 weight rows of a wave's columns
-constexpr int kChunk = 4;                                   // steps whose scales are loaded together
+constexpr int kTiledWaves = 4, kTiledThreads = kTiledWaves * kWave;
+constexpr int kWaveCols = 64;
+constexpr int kTiledCols = kWaveCols * kTiledWaves;
+constexpr int kWRow = kTiledCols / 2;                       // bytes of a weight row
+constexpr int kSubBytes = kStepRows * kWRow;                // 32 weight rows
+constexpr int kXRows = 8 * kTiledWaves;                     // rows of one copy of every wave
+constexpr int kWCopies = 2;                                 // of a wave and step
+constexpr int kBlocks = kTiledCols / kBlock;                // scales of a weight row
+constexpr int kScales = kBlocks * kStep;                    // of a step: a byte each, then fp32
 
-// What weight rows past N are multiplied with.
+// What weight rows past N and rows past the tile are multiplied with.
 __device__ const uint4_t kZeros = {0, 0, 0, 0};
 
-template <int WM_, int WK_, int MT_, int STAGES, int PER_CU>
+template <int MT_, int STAGES, int PER_CU>
 struct Tiling {
-    static constexpr int kPerCu = PER_CU;
-    static constexpr int WM = WM_, WK = WK_, MT = MT_, kStages = STAGES;
-    static constexpr int BM = 16 * MT * WM, BK = kWaveCols * WK;
-    static constexpr int kWaves = WM * WK, kThreads = kWaves * kWave;
-    static constexpr int kXBytes = BM * kXRow, kStage = kXBytes + 2 * WK * kSubBytes;
-    static constexpr int kXRows = 8 * kWaves;               // rows of one copy of every wave
-    static constexpr int kXCopies = BM / kXRows, kWCopies = 4 / WM;
-    static constexpr int kBlocks = 4 * WK;                  // scales of a weight row
-    static constexpr int kHeld = 4 / WM;                    // of them a thread's
-    static constexpr int kScales = kBlocks * kStep * 4;
-    static constexpr int kFlags = STAGES * kStage + 2 * kScales;
+    static constexpr int MT = MT_, kStages = STAGES, kPerCu = PER_CU, BM = 16 * MT;
+    static constexpr int kXBytes = BM * kXRow, kStage = kXBytes + 2 * kSubBytes;
+    static constexpr int kXCopies = BM / kXRows;            // of a wave and step
+    static constexpr int kBytes = kStages * kStage + 2 * kScales * 4, kFlags = kBytes + kStages * kScales;
     static constexpr int kLds = kFlags + 16;
-    static_assert(BM % kXRows == 0 && kXRows % 16 == 0, "a lane's copies share their swizzle");
+    static_assert(BM % kXRows == 0, "whole copies");
     static_assert(kLds * PER_CU <= 160 * 1024, "blocks fit a CU");
 };
 
 __device__ __forceinline__ int x_swizzle(int m) { return (m >> 1) & 7; }
-// Place of the scale of weight row n (of 64) in the row of block b: the four blocks and four
-// lane groups of a wave's read meet different banks.
-__device__ __forceinline__ int scale_at(int b, int n) {
-    return b * kStep + (n ^ ((b & 1) << 2) ^ ((b & 2) << 4));
-}
+__device__ __forceinline__ int w_swizzle(int g) { return g & 2; }
+// Place of the scale of weight row n (of 64) in block b: two blocks and four lane groups that are
+// read together meet different banks.
+__device__ __forceinline__ int scale_at(int b, int n) { return b * kStep + (n ^ ((b & 1) << 2)); }
 
 // Byte C of a weight row's word, columns 2C and 2C + 1, as a pair of 16-bit values.
 template <int C>
@@ -273,29 +289,18 @@ template <int C>
 __device__ __forceinline__ uint32_t pair(uint32_t w, float s, BF16) {
     return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, C));
 }
-template <int C, typename T>
-__device__ __forceinline__ void columns(const uint32_t (&w)[8], const float (&s)[8], T t,
-                                        uint4_t& even, uint4_t& odd) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t a = pair<C>(w[2 * i], s[2 * i], t), b = pair<C>(w[2 * i + 1], s[2 * i + 1], t);
-        even[i] = low_halves(a, b);
-        odd[i] = high_halves(a, b);
-    }
-}
 
 template <typename T, class C, bool WIDE>
-__global__ __launch_bounds__(C::kThreads, C::kPerCu * C::kWaves / 4) void tiled_grad_kernel(GradArgs a) {
+__global__ __launch_bounds__(kTiledThreads, C::kPerCu) void tiled_grad_kernel(GradArgs a) {
     constexpr bool kIsF16 = __is_same(T, F16);
-    constexpr int MT = C::MT;
-    constexpr int kAsync = (WIDE ? C::kXCopies : 0) + C::kWCopies;  // copies in flight, a wave and step
+    constexpr int MT = C::MT, kStages = C::kStages;
+    constexpr int kAsync = (WIDE ? C::kXCopies : 0) + kWCopies;     // in flight, of a wave and step
     typedef typename T::vec8 vec8;
     __shared__ __align__(1024) char lds[C::kLds];
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const int wm = wave / C::WK, wk = wave % C::WK;
     const int r = lane & 15, g = lane >> 4;
-    const int nt = (a.K + C::BK - 1) / C::BK;
+    const int nt = (a.K + kTiledCols - 1) / kTiledCols;
 
     // Tile of this block.  Grouped: column blocks innermost; the XCDs share the tiles in use.
     // Dense: bands of kBand row tiles, row tiles innermost.
@@ -329,337 +334,402 @@ __global__ __launch_bounds__(C::kThreads, C::kPerCu * C::kWaves / 4) void tiled_
         nb = in_band / high;
     }
     if (t.rows <= 0) return;
-    const int k0 = nb * C::BK;
+    const int k0 = nb * kTiledCols;
     const int KB = a.K / kBlock, row_bytes = a.K / 2;
     const int total = (a.N + kStep - 1) / kStep, step0 = slice * a.steps;
     const int steps = t.expert < 0 ? 0 : min(a.steps, total - step0);
     const int64_t expert_row = (int64_t)max(t.expert, 0) * a.N;
     const uint32_t base = lds_address(lds);
 
-    // Copies of dY: wave w, copy c: the 8 rows from (c * kWaves + w) * 8 on.
+    // Copies: a base that moves with the steps and a lane's offset that does not.
+    // dY: wave w, copy c: the 8 rows from (c * kTiledWaves + w) * 8 on.
     const int x_row = wave * 8 + lane / 8, x_chunk = (lane & 7) ^ x_swizzle(x_row);
-    const uint16_t* xp = a.dY + (int64_t)(t.row0 + x_row) * a.y_stride + step0 * kStep + x_chunk * 8;
-    // Of codes: 16 places of 64 bytes, place p of 32 rows being row 8 (p % 4) + p / 4; copy j of a
-    // wave lies 4 (j % 2) + 32 (j / 2) rows behind its first.  Columns past K are not stored: they
-    // read the row's first.
-    const int q0 = wave * C::kWCopies;
-    const int w_col = (k0 + q0 / 4 * kWaveCols) / 2 + (lane & 3) * 16;
-    const int w_row = (q0 >> 1 & 1) * kStepRows + 8 * (lane / 4 & 3) + lane / 16;
-    const uint8_t* wp = a.codes + (expert_row + step0 * kStep + w_row) * row_bytes +
-                        (w_col < row_bytes ? w_col : 0);
-    auto copy = [&](int s) {
-        const uint32_t to = __builtin_amdgcn_readfirstlane(s % C::kStages * C::kStage);
+    const uint16_t* x_base = a.dY + t.row0 * a.y_stride + (int64_t)step0 * kStep;
+    const uint32_t x_off = (uint32_t)(x_row * (uint32_t)a.y_stride + x_chunk * 8) * 2;
+    const int64_t x_next = kXRows * a.y_stride;             // from copy to copy
+    // Codes: copy j of wave w takes the eight places from 8 ((2 w + j) % 4) on of half w / 2 of
+    // the step.  Columns past K are not stored: they read the block's first.
+    const int w_g = lane / 8 & 3, w_chunk = (lane & 7) ^ w_swizzle(w_g);
+    const int w_row = (wave >> 1) * kStepRows + 4 * (wave & 1) + 8 * w_g + lane / 32;   // j: + 2 j
+    const uint8_t* w_base = a.codes + (expert_row + (int64_t)step0 * kStep) * row_bytes + k0 / 2;
+    const uint32_t w_off = (uint32_t)w_row * row_bytes + (k0 / 2 + w_chunk * 16 < row_bytes ? w_chunk * 16 : 0);
+    // Scales: wave w takes those of half w % 2 of the step's rows, four blocks a lane, where they
+    // stand on words (two waves bring the same: a copy for part of a wave costs a branch).
+    const bool words = KB % 4 == 0 && (uintptr_t)a.scales % 4 == 0;
+    const int kb0 = k0 / kBlock, s_row0 = (wave & 1) * kStepRows;
+    const uint32_t s_off = (uint32_t)(s_row0 + lane / 2) * KB + (kb0 + (lane & 1) * 4 < KB ? (lane & 1) * 4 : 0);
+    auto copy_scales = [&](int s) {
+        if (!words || s >= steps) return;
         const int n0 = (step0 + s) * kStep;
-        const bool tail = n0 + kStep > a.N;
-        auto copy_x = [&](int c) {
-            const uint32_t at = to + (c * C::kXRows + wave * 8) * kXRow;
-            const int n = n0 + x_chunk * 8;
-            const bool live = x_row + c * C::kXRows < t.rows;       // others are not stored
-            const uint16_t* p = xp + c * C::kXRows * a.y_stride;
-            if constexpr (WIDE) {
-                copy16(live && !(tail && n >= a.N) ? (const void*)p : &kZeros, base + at);
-            } else {
-                uint4_t v = {0, 0, 0, 0};
+        uint32_t off = s_off;                               // rows past N: the last row's
+        if (n0 + kStep > a.N) off -= (uint32_t)max(n0 + s_row0 + lane / 2 - (a.N - 1), 0) * KB;
+        copy4(a.scales + (expert_row + n0) * KB + kb0, off,
+              __builtin_amdgcn_readfirstlane(base + C::kBytes + s % kStages * kScales + s_row0 * kBlocks));
+    };
+    uint32_t to = 0;                                        // LDS offset of the copied stage
+    auto copy = [&](int s) {
+        const int n0 = (step0 + s) * kStep;
+        const uint32_t x_to = base + to + wave * 8 * kXRow;
+        const uint32_t w_to = base + to + C::kXBytes + wave * 2 * 8 * kWRow;
+        if (WIDE && t.rows == C::BM && n0 + kStep <= a.N) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (live && n + i < a.N) v[i / 2] |= (uint32_t)p[i] << (16 * (i & 1));
-                *(uint4_t*)(lds + at + lane * 16) = v;
-            }
-        };
-        if constexpr (WIDE) {
+            for (int c = 0; c < C::kXCopies; ++c)
+                copy16(x_base + c * x_next, x_off, x_to + c * kXRows * kXRow);
 #pragma unroll
-            for (int c = 0; c < C::kXCopies; ++c) copy_x(c);
+            for (int j = 0; j < kWCopies; ++j)
+                copy16(w_base + 2 * j * row_bytes, w_off, w_to + j * 8 * kWRow);
         } else {
-#pragma unroll 1
-            for (int c = 0; c < C::kXCopies; ++c) copy_x(c);
-        }
-        xp += kStep;
+            int l = lane;                                   // for no register to stay taken
+            asm volatile("" : "+v"(l));
+            const int x_row = wave * 8 + l / 8, x_chunk = (l & 7) ^ x_swizzle(x_row);
+            const int w_row = (wave >> 1) * kStepRows + 4 * (wave & 1) + 8 * (l / 8 & 3) + l / 32;
+            auto copy_x = [&](int c) {
+                const int n = n0 + x_chunk * 8;
+                const bool live = x_row + c * kXRows < t.rows;
+                const uint16_t* p = x_base + c * x_next + x_row * a.y_stride + x_chunk * 8;
+                if constexpr (WIDE) {
+                    copy16(live && n < a.N ? (const void*)p : &kZeros, x_to + c * kXRows * kXRow);
+                } else {
+                    uint4_t v = {0, 0, 0, 0};
 #pragma unroll
-        for (int j = 0; j < C::kWCopies; ++j) {
-            int row = 4 * (j & 1) + kStepRows * (j >> 1);
-            // Rows past N: the last row's codes.
-            if (tail) row = min(row, a.N - 1 - n0 - w_row);
-            copy16(wp + (int64_t)row * row_bytes,
-                   base + to + C::kXBytes + (q0 + j) * (kSubBytes / 2));
+                    for (int i = 0; i < 8; ++i)
+                        if (live && n + i < a.N) v[i / 2] |= (uint32_t)p[i] << (16 * (i & 1));
+                    *(uint4_t*)(lds + to + (c * kXRows + wave * 8) * kXRow + l * 16) = v;
+                }
+            };
+            if constexpr (WIDE) {
+#pragma unroll
+                for (int c = 0; c < C::kXCopies; ++c) copy_x(c);
+            } else {
+#pragma unroll 1
+                for (int c = 0; c < C::kXCopies; ++c) copy_x(c);
+            }
+#pragma unroll
+            for (int j = 0; j < kWCopies; ++j) {            // rows past N: the last row's codes
+                const int row = min(2 * j, a.N - 1 - n0 - w_row);
+                copy16(w_base + w_off + (int64_t)row * row_bytes, w_to + j * 8 * kWRow);
+            }
         }
-        wp += (int64_t)kStep * row_bytes;
+        x_base += kStep;
+        w_base += (int64_t)kStep * row_bytes;
+        to = to + C::kStage == kStages * C::kStage ? 0 : to + C::kStage;
     };
 
-    // Scales: a thread holds those of kHeld blocks of one weight row of each of kChunk steps.
-    constexpr int kPerRow = C::kBlocks / C::kHeld;          // threads of a weight row
-    const int s_row = threadIdx.x / kPerRow, s_block = threadIdx.x % kPerRow * C::kHeld;
-    const int kb0 = k0 / kBlock + s_block;
-    uint32_t held[kChunk];
-    auto load_scales = [&](int s) {                         // of steps s .. s + kChunk - 1
-#pragma unroll
-        for (int c = 0; c < kChunk; ++c) {
-            const int n = (step0 + s + c) * kStep + s_row;
-            held[c] = 0x7F7F7F7Fu;                          // past N and K: 1
-            if (n >= a.N) continue;
-            const uint8_t* p = a.scales + (expert_row + n) * KB + kb0;
-            if (kb0 + C::kHeld <= KB) {
-                __builtin_memcpy(&held[c], p, C::kHeld);    // any byte
-            } else {
-#pragma unroll
-                for (int b = 0; b < C::kHeld; ++b)
-                    if (kb0 + b < KB) held[c] = (held[c] & ~(255u << 8 * b)) | (uint32_t)p[b] << 8 * b;
-            }
-        }
-    };
+    // Scales as fp32: two blocks of a weight row a thread.
     bool far = false;
-    float* scales = (float*)(lds + C::kStages * C::kStage);
+    float* scales = (float*)(lds + kStages * C::kStage);
     volatile int* wide_at = (volatile int*)(lds + C::kFlags);   // of even and odd steps: the last
                                                                 // one outside fp16's range
-    auto store_scales = [&](int s) {
+    auto convert_scales = [&](int s) {
+        if (s >= steps) return;
+        const int s_row = threadIdx.x / 4, s_block = threadIdx.x % 4 * 2;
+        const int n = (step0 + s) * kStep + s_row;
+        uint32_t v;
+        if (words) {
+            v = *(const uint16_t*)(lds + C::kBytes + s % kStages * kScales + threadIdx.x * 2);
+        } else {                                            // past K: not stored
+            const uint8_t* row = a.scales + (expert_row + min(n, a.N - 1)) * KB;
+            const int kb = kb0 + s_block;
+            v = row[min(kb, KB - 1)] | (uint32_t)row[min(kb + 1, KB - 1)] << 8;
+        }
+        if (n >= a.N) v = 0x7F7F;                           // past N: 1
         bool out = false;
 #pragma unroll
-        for (int b = 0; b < C::kHeld; ++b) {
-            const uint32_t byte = held[0] >> 8 * b & 255;
+        for (int b = 0; b < 2; ++b) {
+            const uint32_t byte = v >> 8 * b & 255;
             out = out || !f16_scale_ok(byte);
             far = far || byte >= kFarScale;
-            scales[(s & 1) * (C::kScales / 4) + scale_at(s_block + b, s_row)] = scale_value(byte);
+            scales[(s & 1) * kScales + scale_at(s_block + b, s_row)] = scale_value(byte);
         }
         if (kIsF16 && out) wide_at[s & 1] = s;
-#pragma unroll
-        for (int c = 0; c + 1 < kChunk; ++c) held[c] = held[c + 1];
-        if (s % kChunk == kChunk - 1) load_scales(s + 1);
     };
 
-    // Operands of 32 weight rows.
-    struct Sub {
-        uint32_t w[8];
-        float s[8];
-        vec8 x[MT];
-    };
-    const int x_at = (wm * MT * 16 + r) * kXRow, swizzle = x_swizzle(r);
-    const int w_at = C::kXBytes + wk * 2 * kSubBytes + g * 64 + r * 4;
-    const int block = wk * 4 + r / 4;
-    auto load_w = [&](Sub& d, int s, int sub) {
-        const char* stage = lds + s % C::kStages * C::kStage;
+    // Operands: of weights the words (four columns) and scales of the lane's eight rows, then a
+    // pair of columns at a time; of dY a fragment per row tile.
+    uint32_t w[8];
+    float sc[8];
+    vec8 x[MT];
+    uint4_t f[2][2];
+    float4_t acc[MT][4] = {};
+    const int x_at = r * kXRow + (g ^ x_swizzle(r)) * 16;   // half 1's is 64 bytes on or back
+    const int w_at = C::kXBytes + g * kWRow + ((wave * 2) ^ w_swizzle(g)) * 16 + r * 2;
+    const int s_at = scale_at(wave * 2 + r / 8, 8 * g);
+    auto load_w = [&](uint32_t stage, int s, int sub) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            d.w[i] = *(const uint32_t*)(stage + w_at + sub * kSubBytes + i * 256);
-        const float* sc = scales + (s & 1) * (C::kScales / 4);
+            w[i] = *(const uint16_t*)(lds + stage + w_at + sub * kSubBytes + i * 4 * kWRow);
+        const float* from = scales + (s & 1) * kScales + sub * kStepRows;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const float4_t v = *(const float4_t*)&sc[scale_at(block, sub * kStepRows + 8 * g + 4 * h)];
+            const float4_t v = *(const float4_t*)(from + (s_at ^ h * 4));
 #pragma unroll
-            for (int i = 0; i < 4; ++i) d.s[4 * h + i] = v[i];
+            for (int i = 0; i < 4; ++i) sc[4 * h + i] = v[i];
         }
     };
-    auto load_x = [&](int s, int sub, int m) {
-        const char* stage = lds + s % C::kStages * C::kStage;
-        return *(const vec8*)(stage + x_at + m * 16 * kXRow + ((4 * sub + g) ^ swizzle) * 16);
+    auto load_x = [&](uint32_t stage, int sub, int m) {
+        return *(const vec8*)(lds + stage + (x_at ^ sub * 64) + m * 16 * kXRow);
     };
-    auto load = [&](Sub& d, int s, int sub) {
-        load_w(d, s, sub);
-#pragma unroll
-        for (int m = 0; m < MT; ++m) d.x[m] = load_x(s, sub, m);
-    };
-    float4_t acc[MT][8] = {};
-    // The products of d's pair C of columns (even and odd in f), while the next pair, next.w's byte
-    // (C + 1) % 4, is converted.
-    uint4_t f[2][2];
-    auto convert = [&](auto c, const Sub& d) {
-        constexpr int CC = decltype(c)::value;
-        columns<CC>(d.w, d.s, T(), f[CC & 1][0], f[CC & 1][1]);
-    };
-    auto multiply = [&](auto c, const Sub& d, const Sub& next) {
-        constexpr int CC = decltype(c)::value;
-        convert(Int<(CC + 1) % 4>(), next);
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-                acc[m][2 * CC + h] = T::mfma16(__builtin_bit_cast(vec8, f[CC & 1][h]), d.x[m],
-                                               acc[m][2 * CC + h]);
-        __builtin_amdgcn_sched_barrier(0);
+    // Weight rows 2i and 2i + 1 of the columns 2c and 2c + 1.
+    auto convert = [&](auto pair_of, auto rows, auto type) {
+        constexpr int c = decltype(pair_of)::value, i = decltype(rows)::value;
+        const uint32_t p = pair<c>(w[2 * i], sc[2 * i], type);
+        const uint32_t q = pair<c>(w[2 * i + 1], sc[2 * i + 1], type);
+        f[c][0][i] = low_halves(p, q);
+        f[c][1][i] = high_halves(p, q);
     };
 
     if (steps > 0) {
         if (threadIdx.x < 2) wide_at[threadIdx.x] = -1;
         __syncthreads();
-        load_scales(0);
-        store_scales(0);
 #pragma unroll
-        for (int s = 0; s < C::kStages; ++s)
+        for (int s = 0; s < kStages; ++s) {
             if (s < steps) copy(s);
+            copy_scales(s);
+        }
         wait_copies<0>();
-        // To step s + 1, when a wave has all of step s in registers.
-        auto advance = [&](int s) {
-            if (s + 1 >= steps) return;
-            store_scales(s + 1);
-            if (s + C::kStages <= steps) wait_copies<(C::kStages - 2) * kAsync>();
-            else wait_copies<0>();
-            if (s + C::kStages < steps) copy(s + C::kStages);
+        convert_scales(0);
+        convert_scales(1);
+        __syncthreads();
+        copy_scales(kStages);                               // where those of step 0 stood
+        // To step s + 1, when a wave has all of step s in registers: its tile is free for the copy
+        // kStages on, its scales for those of step s + 2.
+        auto next_step = [&](int s) {
+            if (s + kStages > steps) wait_copies<0>();
+            else if (s + kStages + 1 <= steps && words) wait_copies<(kStages - 2) * (kAsync + 1)>();
+            else wait_copies<(kStages - 2) * kAsync>();
         };
-        Sub d[2];
-        load(d[0], 0, 0);
-        convert(Int<0>(), d[0]);
-        int s = 0;
+        uint32_t stage = 0;
+        load_w(0, 0, 0);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) x[m] = load_x(0, 0, m);
+        each_of([&](auto i) { convert(Int<0>(), i, T()); }, Int<4>());
+        // The products of a pair of columns over the row tiles, while the next pair is converted:
+        // pair 1 of these weight rows, or pair 0 of the next ones, which are half `sub` of step s
+        // at `stage` and are read meanwhile, dY's fragments as their last use passes.
+        auto products = [&](auto pair_of, uint32_t stage, int s, int sub) {
+            constexpr int c = decltype(pair_of)::value;
+            if constexpr (c == 1) load_w(stage, s, sub);
+            each_of([&](auto mm) {
+                constexpr int m = decltype(mm)::value;
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    acc[m][2 * c + h] =
+                        T::mfma16(__builtin_bit_cast(vec8, f[c][h]), x[m], acc[m][2 * c + h]);
+                if constexpr (c == 1) x[m] = load_x(stage, sub, m);
+                // The four units of the next pair, behind the reads of their weights.
+                constexpr int F = MT / 2, kLeft = MT - F;
+                if constexpr (m >= F)
+                    units<(m - F) * 4 / kLeft, (m - F + 1) * 4 / kLeft>(
+                        [&](auto i) { convert(Int<1 - c>(), i, T()); });
+                __builtin_amdgcn_sched_barrier(0);
+            }, Int<MT>());
+        };
+        int s = 0, wide = kIsF16 ? wide_at[0] : -1;
         for (; s < steps; ++s) {
-            if (kIsF16 && __builtin_amdgcn_readfirstlane(wide_at[s & 1]) == s) break;
-            load(d[1], s, 1);
-            multiply(Int<0>(), d[0], d[0]);
-            multiply(Int<1>(), d[0], d[0]);
-            multiply(Int<2>(), d[0], d[0]);
-            multiply(Int<3>(), d[0], d[1]);
-            advance(s);
-            load(d[0], s + 1, 0);                   // past the last step: not used
-            multiply(Int<0>(), d[1], d[1]);
-            multiply(Int<1>(), d[1], d[1]);
-            multiply(Int<2>(), d[1], d[1]);
-            multiply(Int<3>(), d[1], d[0]);
+            if (kIsF16 && __builtin_amdgcn_readfirstlane(wide) == s) break;
+            products(Int<0>(), 0, 0, 0);
+            products(Int<1>(), stage, s, 1);
+            products(Int<0>(), 0, 0, 0);
+            __builtin_amdgcn_s_setprio(0);
+            if (s + 1 < steps) next_step(s);
+            stage = stage + C::kStage == kStages * C::kStage ? 0 : stage + C::kStage;
+            if (s + kStages < steps) copy(s + kStages);
+            copy_scales(s + 1 + kStages);                   // where those of step s + 1 stood
+            convert_scales(s + 2);
+            if (kIsF16) wide = wide_at[(s + 1) & 1];
+            __builtin_amdgcn_s_setprio(1);
+            products(Int<1>(), stage, s + 1, 0);            // past the last step: not used
         }
         // From the first step with weights outside fp16's range on: weights are exact in bf16,
         // dY is the sum of two bf16 values.
         for (; kIsF16 && s < steps; ++s) {
 #pragma unroll 1
             for (int sub = 0; sub < 2; ++sub) {
-                load_w(d[0], s, sub);
-                auto pairs = [&](auto c) {
-                    constexpr int CC = decltype(c)::value;
-                    uint4_t w[2];
-                    columns<CC>(d[0].w, d[0].s, BF16(), w[0], w[1]);
+                load_w(stage, s, sub);
+                each_of([&](auto i) {
+                    convert(Int<0>(), i, BF16());
+                    convert(Int<1>(), i, BF16());
+                }, Int<4>());
 #pragma unroll
-                    for (int m = 0; m < MT; ++m) {
-                        bf168_t hi, lo;
-                        split_bf16(__builtin_bit_cast(half8_t, load_x(s, sub, m)), hi, lo);
+                for (int m = 0; m < MT; ++m) {
+                    bf168_t hi, lo;
+                    split_bf16(__builtin_bit_cast(half8_t, load_x(stage, sub, m)), hi, lo);
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            float4_t& to = acc[m][2 * CC + h];
-                            to = BF16::mfma16(__builtin_bit_cast(bf168_t, w[h]), hi, to);
-                            to = BF16::mfma16(__builtin_bit_cast(bf168_t, w[h]), lo, to);
-                        }
-                        __builtin_amdgcn_sched_barrier(0);
+                    for (int j = 0; j < 4; ++j) {
+                        const bf168_t v = __builtin_bit_cast(bf168_t, f[j / 2][j % 2]);
+                        acc[m][j] = BF16::mfma16(v, hi, acc[m][j]);
+                        acc[m][j] = BF16::mfma16(v, lo, acc[m][j]);
                     }
-                };
-                pairs(Int<0>()), pairs(Int<1>()), pairs(Int<2>()), pairs(Int<3>());
+                    __builtin_amdgcn_sched_barrier(0);
+                }
             }
-            advance(s);
+            if (s + 1 < steps) next_step(s);
+            stage = stage + C::kStage == kStages * C::kStage ? 0 : stage + C::kStage;
+            if (s + kStages < steps) copy(s + kStages);
+            copy_scales(s + 1 + kStages);
+            convert_scales(s + 2);
         }
         wait_copies<0>();
         if (__syncthreads_or(far)) {
             // Weights that bf16 does not hold: the block's sums again, in quarters, straight from
             // global memory.
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) acc[m][j] = (float4_t){0, 0, 0, 0};
-            const int col = min(k0 + wk * kWaveCols + 8 * r, a.K - 8);
+            int l = lane;
+            asm volatile("" : "+v"(l));
+            const int r = l & 15, g = l >> 4;
+            const int col = min(k0 + wave * kWaveCols + 4 * r, a.K - 4);
             const int last = min((step0 + steps) * kStep, a.N);
-            auto row_tile = [&](auto tile) {                // a row tile at a time: registers
+            each_of([&](auto tile) {                        // a row tile at a time: registers
                 constexpr int m = decltype(tile)::value;
-                const int row = min((wm * MT + m) * 16 + r, t.rows - 1);
-                const uint16_t* from = a.dY + (t.row0 + row) * a.y_stride;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[m][j] = (float4_t){0, 0, 0, 0};
+                const uint16_t* from = a.dY + (t.row0 + min(m * 16 + r, t.rows - 1)) * a.y_stride;
 #pragma unroll 1
                 for (int n0 = step0 * kStep; n0 < last; n0 += kStepRows) {
-                    uint32_t w[8], sb[8];
-                    uint4_t x = {0, 0, 0, 0}, q[8];
+                    uint32_t word[8], sb[8];
+                    uint4_t v = {0, 0, 0, 0}, q[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const int n = n0 + 8 * g + i, at = min(n, a.N - 1);
-                        const int64_t weight = expert_row + at;
-                        w[i] = *(const uint32_t*)(a.codes + weight * row_bytes + col / 2);
-                        sb[i] = a.scales[weight * KB + col / kBlock];
-                        const uint32_t v = from[at];
+                        const int64_t row = expert_row + at;
+                        word[i] = *(const uint16_t*)(a.codes + row * row_bytes + col / 2);
+                        sb[i] = a.scales[row * KB + col / kBlock];
+                        const uint32_t e = from[at];
                         if (n >= a.N) sb[i] = 127;
-                        x[i / 2] |= (n < a.N ? v : 0) << (16 * (i & 1));
+                        v[i / 2] |= (n < a.N ? e : 0) << (16 * (i & 1));
                     }
-                    turn8<BF16>(w, [&](uint32_t v, int i) { return quarter8(v, sb[i]); }, q);
-                    bf168_t hi = __builtin_bit_cast(bf168_t, x), lo;
-                    if constexpr (kIsF16) split_bf16(__builtin_bit_cast(half8_t, x), hi, lo);
+                    turn8<BF16>(word, [&](uint32_t u, int i) { return quarter8(u, sb[i]); }, q);
+                    bf168_t hi = __builtin_bit_cast(bf168_t, v), lo;
+                    if constexpr (kIsF16) split_bf16(__builtin_bit_cast(half8_t, v), hi, lo);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const bf168_t v = __builtin_bit_cast(bf168_t, q[j]);
-                        acc[m][j] = BF16::mfma16(v, hi, acc[m][j]);
-                        if constexpr (kIsF16) acc[m][j] = BF16::mfma16(v, lo, acc[m][j]);
+                    for (int j = 0; j < 4; ++j) {
+                        const bf168_t u = __builtin_bit_cast(bf168_t, q[j]);
+                        acc[m][j] = BF16::mfma16(u, hi, acc[m][j]);
+                        if constexpr (kIsF16) acc[m][j] = BF16::mfma16(u, lo, acc[m][j]);
                     }
                 }
-            };
-            static_assert(MT == 1 || MT == 2 || MT == 4, "every row tile once");
-            row_tile(Int<0>());
-            if constexpr (MT > 1) row_tile(Int<1>());
-            if constexpr (MT > 2) row_tile(Int<2>()), row_tile(Int<MT - 1>());
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) acc[m][j] *= 4.0f;
+                for (int j = 0; j < 4; ++j) acc[m][j] *= 4.0f;
+            }, Int<MT>());
         }
     }
 
     // Results: lane l holds row l % 16 of dX and, in register i of acc[m][j], the column
-    // 8 (4 g + i) + j: 32 neighbouring columns.
-    const int col = k0 + wk * kWaveCols + 32 * g;
+    // 4 (4 g + i) + j: 16 neighbouring columns.
+    int l = lane;
+    asm volatile("" : "+v"(l));
+    const int col = k0 + wave * kWaveCols + 16 * (l >> 4);
     if (col >= a.K) return;
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-        const int row = (wm * MT + m) * 16 + r;
+        const int row = m * 16 + (l & 15);
         if (row >= t.rows) continue;
         const int64_t at = (int64_t)(t.row0 + row) * a.K + col;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int h = 0; h < 2; ++h) {
             float v[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = acc[m][j][i];
+            for (int j = 0; j < 8; ++j) v[j] = acc[m][j % 4][2 * h + j / 4];
             if (a.part != nullptr) {
-                float* out = a.part + (int64_t)slice * a.R * a.K + at + 8 * i;
+                float* out = a.part + (int64_t)slice * a.R * a.K + at + 8 * h;
                 __builtin_memcpy(__builtin_assume_aligned(out, 16), v, 32);
             } else {
                 uint16_t o[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) o[j] = T::store(v[j]);
-                __builtin_memcpy(__builtin_assume_aligned(a.dX + at + 8 * i, 16), o, 16);
+                __builtin_memcpy(__builtin_assume_aligned(a.dX + at + 8 * h, 16), o, 16);
             }
         }
     }
 }
 
-typedef Tiling<2, 2, 4, 3, 2> Large;        // 128 x 256
+typedef Tiling<8, 3, 2> Large;      // 128 x 256
+typedef Tiling<6, 3, 2> Mid;        // 96 x 256
+typedef Tiling<4, 3, 2> Medium;     // 64 x 256
+typedef Tiling<2, 3, 3> Low;        // 32 x 256
 
 template <class C>
 void launch(GradArgs a, DType dt, hipStream_t stream) {
-    const bool wide = (uintptr_t)a.dY % 16 == 0 && a.N % 8 == 0 && (a.y_stride % 8 == 0 || a.R == 1);
-    const int64_t nt = (a.K + C::BK - 1) / C::BK;
+    // The offset of a copy's rows has 32 bits.
+    const bool wide = (uintptr_t)a.dY % 16 == 0 && a.N % 8 == 0 &&
+                      (a.R == 1 || (a.y_stride % 8 == 0 && a.y_stride <= 1 << 25));
+    const int64_t nt = (a.K + kTiledCols - 1) / kTiledCols;
     const int64_t slots = a.offsets ? tile_slots(a.R, a.E, C::BM) : (a.R + C::BM - 1) / C::BM;
     const int64_t blocks = slots * nt * a.slices;
     for (a.first = 0; a.first < blocks; a.first += kMaxGrid) {
         const unsigned grid = (unsigned)(blocks - a.first < kMaxGrid ? blocks - a.first : kMaxGrid);
         if (dt == kF16 && wide)
-            tiled_grad_kernel<F16, C, true><<<grid, C::kThreads, 0, stream>>>(a);
+            tiled_grad_kernel<F16, C, true><<<grid, kTiledThreads, 0, stream>>>(a);
         else if (dt == kF16)
-            tiled_grad_kernel<F16, C, false><<<grid, C::kThreads, 0, stream>>>(a);
+            tiled_grad_kernel<F16, C, false><<<grid, kTiledThreads, 0, stream>>>(a);
         else if (wide)
-            tiled_grad_kernel<BF16, C, true><<<grid, C::kThreads, 0, stream>>>(a);
+            tiled_grad_kernel<BF16, C, true><<<grid, kTiledThreads, 0, stream>>>(a);
         else
-            tiled_grad_kernel<BF16, C, false><<<grid, C::kThreads, 0, stream>>>(a);
+            tiled_grad_kernel<BF16, C, false><<<grid, kTiledThreads, 0, stream>>>(a);
     }
 }
 
 // Kernel and N slices.
-enum Kernel { kStream, kLarge };
+//   Experts, by rows per expert on average (all rows / experts), as measured for 64 experts of
+//   3584 x 4096; other counts and sizes follow the same borders (us):
+//     rows     stream   Low   Medium   Mid   Large
+//     2           117   135      202   224     248
+//     16          168   143      214   227     252
+//     32          260   197      207   230     256
+//     64          443   274      277   243     266
+//     96                372      312   313     283
+//     320              1014      788   681     670
+//   Dense: up to 16 rows the streaming kernel; else the tiling and the slices that the times below
+//   say are fastest.
+enum Kernel { kStream, kLow, kMedium, kMid, kLarge };
 struct Choice {
     Kernel kernel;
     int slices, steps;
 };
+// A step of 64 weight rows takes kOne us with a block on a CU and kTwo with two of them (M x 4096,
+// 8192 weight rows); a launch begins and ends with the time of about three.
+struct Cost {
+    Kernel kernel;
+    int rows;
+    double one, two;
+};
+constexpr Cost kCosts[] = {{kLarge, Large::BM, 1.20, 1.54}, {kMid, Mid::BM, 1.07, 1.33},
+                           {kMedium, Medium::BM, 0.93, 1.08}, {kLow, Low::BM, 0.83, 0.87}};
+
 Choice choose(int64_t R, int64_t E, int64_t N, int64_t K, bool grouped, bool split) {
-    Choice c{R > 32 * E ? kLarge : kStream, 1, 0};
-    const int rows = c.kernel == kStream ? kStepRows : kStep;
-    const int64_t total = N > 0 ? (N + rows - 1) / rows : 1;
-    c.steps = (int)total;
-    if (grouped || !split) return c;
-    // As many as give every CU two blocks, of at least four steps a wave (tiled: eight).
-    const int64_t blocks = c.kernel == kStream ? (R + kTile - 1) / kTile * ((K + kCols - 1) / kCols)
-                                               : (R + Large::BM - 1) / Large::BM *
-                                                     ((K + Large::BK - 1) / Large::BK);
-    const int64_t least = c.kernel == kStream ? 4 * kWaves : 8;
-    int64_t s = 512 / blocks;
-    if (s > total / least) s = total / least;
-    if (s > 1) {
-        c.steps = (int)((total + s - 1) / s);
-        c.slices = (int)((total + c.steps - 1) / c.steps);
+    const int64_t steps = N > 0 ? (N + kStep - 1) / kStep : 1;
+    Choice best{kStream, 1, (int)steps};
+    if (grouped ? R < 12 * E : R <= kTile) {
+        const int64_t total = N > 0 ? (N + kStepRows - 1) / kStepRows : 1;
+        best.steps = (int)total;
+        // Slices: as many as give every CU two blocks, of at least four steps a wave.
+        int64_t s = split ? 512 / ((K + kCols - 1) / kCols) : 1;
+        if (s > total / (4 * kWaves)) s = total / (4 * kWaves);
+        if (!grouped && s > 1) {
+            best.steps = (int)((total + s - 1) / s);
+            best.slices = (int)((total + best.steps - 1) / best.steps);
+        }
+        return best;
     }
-    return c;
+    if (grouped) {
+        best.kernel = R < 28 * E ? kLow : R < 52 * E ? kMedium : R < 80 * E ? kMid : kLarge;
+        return best;
+    }
+    double least = 0;
+    for (const Cost& c : kCosts) {
+        const int64_t tiles = (R + c.rows - 1) / c.rows * ((K + kTiledCols - 1) / kTiledCols);
+        for (int64_t s = 1; s <= (split ? 16 : 1) && (s == 1 || steps / s >= 4); ++s) {
+            const int64_t run = (steps + s - 1) / s, slices = (steps + run - 1) / run;
+            const int64_t blocks = tiles * slices, left = blocks % 512;
+            double us = (run + 3) * (double(blocks / 512) * c.two + (left > 256 ? c.two : left > 0 ? c.one : 0));
+            // The slices' sums are written, read and added at about 4 TB/s by a second launch.
+            if (slices > 1) us += 3 + double(slices) * R * K * 8 / 4e6;
+            if (best.kernel == kStream || us < least) {
+                least = us;
+                best = {c.kernel, (int)slices, (int)run};
+            }
+        }
+    }
+    return best;
 }
 
 }  // namespace
@@ -676,6 +746,12 @@ hipError_t launch_grad(GradArgs a, DType dt, float* part, hipStream_t stream) {
     a.part = c.slices > 1 ? part : a.dX32;
     if (c.kernel == kLarge) {
         launch<Large>(a, dt, stream);
+    } else if (c.kernel == kMid) {
+        launch<Mid>(a, dt, stream);
+    } else if (c.kernel == kMedium) {
+        launch<Medium>(a, dt, stream);
+    } else if (c.kernel == kLow) {
+        launch<Low>(a, dt, stream);
     } else {
         const int64_t slots = a.offsets ? tile_slots(a.R, a.E, kTile) : (a.R + kTile - 1) / kTile;
         const dim3 grid = slot_grid((a.K + kCols - 1) / kCols * a.slices, slots);

@@ -37,6 +37,20 @@ __device__ __forceinline__ void copy16(const void* p, uint32_t lds) {
                  : "s"(lds), "v"(p)
                  : "m0", "memory");
 }
+// The same from a base (the same in the wave) and an offset of a lane in bytes.
+__device__ __forceinline__ void copy16(const void* base, uint32_t off, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2"
+                 :
+                 : "s"(lds), "v"(off), "s"(base)
+                 : "m0", "memory");
+}
+// Four bytes per lane, into LDS at lds + 4 * lane.
+__device__ __forceinline__ void copy4(const void* base, uint32_t off, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dword %1, %2"
+                 :
+                 : "s"(lds), "v"(off), "s"(base)
+                 : "m0", "memory");
+}
 // Waits until at most `left` of the wave's loads are in flight and its LDS
 // operations are done, then for the block's other waves.
 template <int LEFT>
