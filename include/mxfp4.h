@@ -259,7 +259,7 @@ int mxfp4_grouped_linear_grad(const void* dY, int dtype, int64_t R, int64_t y_st
  *   loss   out: fp32, one value (0 where C or T' is 0)
  *   counts out: int32 [E + 1]: c_e, and T' in counts[E]
  *   workspace DEVICE, 4-byte aligned, at least moe_balance_workspace_bytes(T, E, k)
- *             bytes (may be NULL for T = 0); no initial contents needed, in use
+ *             bytes (may be NULL where that is 0); no initial contents needed, in use
  *             until the call's work on the stream has finished.
  * A logit of NaN or +infinity makes the loss NaN.  T k <= 2^29. */
 size_t moe_balance_workspace_bytes(int64_t T, int64_t E, int64_t k);

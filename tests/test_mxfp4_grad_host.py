@@ -164,25 +164,26 @@ def test_grouped_linear_grad_refusals(lib):  # noqa: F811
 
 def test_balance_refusals(lib):  # noqa: F811
     size = lib.moe_balance_workspace_bytes
-    need = size(4, 8, 2)
-    assert need > 0 and size(0, 8, 2) == 0
-    for bad in ((-1, 8, 2), (4, 0, 2), (4, 1025, 2), (4, 8, 0), (4, 8, 33), (1 << 25, 8, 2)):
+    need = size(1000, 8, 2)
+    assert need > 0 and size(0, 8, 2) == 0 and size(128, 64, 2) == 0 and size(4, 1024, 2) > 0
+    for bad in ((-1, 8, 2), (1000, 0, 2), (1000, 1025, 2), (1000, 8, 0), (1000, 8, 33), (1 << 25, 8, 2)):
         assert size(*bad) == 0
+    far = 16 * FAKE
 
-    def call(x=A, dt=0, T=4, E=8, st=8, ids=B, k=2, loss=C, n=D, ws=F, wb=need):
+    def call(x=A, dt=0, T=1000, E=8, st=8, ids=B, k=2, loss=C, n=D, ws=far, wb=need):
         return lib.moe_balance(x, dt, T, E, st, ids, k, loss, n, ws, wb, None)
     assert call(dt=3) == INVALID and call(T=-1) == INVALID and call(E=0) == INVALID
     assert call(E=1025, st=1025) == INVALID and call(k=0) == INVALID and call(k=33) == INVALID
     assert call(st=7) == INVALID
     for name in ("x", "ids", "loss", "n"):
         assert call(**{name: None}) == INVALID and call(**{name: G + 1}) == MISALIGNED
-    assert call(x=A + 2, dt=2) == MISALIGNED and call(ws=F + 2) == MISALIGNED
+    assert call(x=A + 2, dt=2) == MISALIGNED and call(ws=far + 2) == MISALIGNED
     assert call(ws=None, wb=0) == INVALID and call(wb=need - 1) == INVALID
     assert call(loss=A) == INVALID and call(n=B) == INVALID and call(loss=D + 32) == INVALID
     assert call(ws=A) == INVALID and call(ws=D) == INVALID
     if not torch.cuda.is_available():
         assert call() == DEVICE and call(T=0, x=None, ids=None, ws=None, wb=0) == DEVICE
-        assert call(loss=D + 36) == DEVICE
+        assert call(T=100, ws=None, wb=0) == DEVICE and call(loss=D + 36) == DEVICE
 
 
 def test_route_grad_refusals(lib):  # noqa: F811

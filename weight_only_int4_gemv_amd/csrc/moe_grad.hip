@@ -22,233 +22,359 @@ struct Of<kBF16> { typedef BF16 tag; };
 template <>
 struct Of<kF32> { typedef F32 tag; };
 
-template <DType DT>
-__device__ __forceinline__ float load(const void* p, int64_t i) {
-    typedef typename Of<DT>::tag T;
-    return T::load(((const typename T::type*)p)[i]);
+// ------------------------------------------------------------ softmax of logits
+//
+// A token takes LANES lanes of a wave, each with PER neighbouring experts: up to 64 experts eight
+// lanes, so that a wave works on eight tokens, reads 16 bytes a lane and sums over a row of lanes
+// with DPP steps.  (65521 tokens of 128 experts: a wave per token with shuffles through LDS takes
+// 36 us for the loss's sums and 35 for the gradient.)
+
+// The value of lane i ^ 1, i ^ 2, then of the other half of 8, of 16, of 32 and of 64 lanes whose
+// own values are alike.
+template <int D>
+__device__ __forceinline__ float other(float v) {
+    const int b = __builtin_bit_cast(int, v);
+    if constexpr (D == 1) return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, b, 0xB1, 0xF, 0xF, true));
+    else if constexpr (D == 2) return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, b, 0x4E, 0xF, 0xF, true));
+    else if constexpr (D == 4) return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, b, 0x141, 0xF, 0xF, true));
+    else if constexpr (D == 8) return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, b, 0x140, 0xF, 0xF, true));
+    else return __shfl_xor(v, D);
+}
+template <int LANES, int D = 1>
+__device__ __forceinline__ float lanes_sum(float v) {
+    if constexpr (D == LANES) return v;
+    else return lanes_sum<LANES, 2 * D>(v + other<D>(v));
+}
+__device__ __forceinline__ float wave_sum(float v) { return lanes_sum<kWave>(v); }
+// NaN aside, which enters by its own exponential.
+template <int LANES, int D = 1>
+__device__ __forceinline__ float lanes_peak(float v) {
+    if constexpr (D == LANES) return v;
+    else return lanes_peak<LANES, 2 * D>(fmaxf(v, other<D>(v)));
 }
 
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-    for (int d = 1; d < kWave; d <<= 1) v += __shfl_xor(v, d);
-    return v;
+// exp(t) for t <= 0 to about an ulp: the product with log2 e in two parts, the low one as a factor
+// 1 + low ln 2.  Below -200 it is 0; a NaN stays.
+__device__ __forceinline__ float exp_down(float t) {
+    t = t < -200.0f ? -200.0f : t;
+    const float h = t * 1.44269502f;
+    const float l = fmaf(t, 1.44269502f, -h) + t * 1.92596299e-8f;
+    const float e = __builtin_amdgcn_exp2f(h);
+    return fmaf(e, l * 0.693147181f, e);
 }
-// The largest value; a NaN counts above every number.
-__device__ __forceinline__ float wave_peak(float v) {
+
+// PER elements from p on, `left` of which are there: others are `fill`.
+template <typename T, int PER>
+__device__ __forceinline__ void load_some(const typename T::type* p, int left, bool wide, float fill,
+                                          float (&v)[PER]) {
+    if (wide && left >= PER) {
+        typename T::type b[PER];
+        __builtin_memcpy(b, __builtin_assume_aligned(p, 16), sizeof(b));
 #pragma unroll
-    for (int d = 1; d < kWave; d <<= 1) {
-        const float o = __shfl_xor(v, d);
-        v = o > v || o != o ? o : v;
+        for (int i = 0; i < PER; ++i) v[i] = T::load(b[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) v[i] = i < left ? T::load(p[i]) : fill;
     }
-    return v;
 }
 
-// exp(l - max) of a token's logits, lane l holding experts l, l + 64, ..., and their sum.  A row
-// without a usable expert (all -infinity) has sum 0.
-template <DType DT, int PER_LANE>
+// exp(l - peak) of a token's logits and their sum.  A row without a usable expert (all -infinity)
+// has sum 0; one with a NaN or +infinity has sum NaN.
+template <int LANES, int PER>
 struct Softmax {
-    float p[PER_LANE], peak, sum;
-    __device__ __forceinline__ void read(const void* logits, int64_t row, int E) {
-        const int lane = threadIdx.x & (kWave - 1);
-        peak = -INFINITY;
+    float p[PER], peak, sum;
+    __device__ __forceinline__ void make() {                // from the logits in p
+        peak = p[0];
 #pragma unroll
-        for (int i = 0; i < PER_LANE; ++i) {
-            const int e = lane + kWave * i;
-            p[i] = e < E ? load<DT>(logits, row + e) : -INFINITY;
-            peak = p[i] > peak || p[i] != p[i] ? p[i] : peak;
-        }
-        peak = wave_peak(peak);
-        float s = 0.0f;
+        for (int i = 1; i < PER; ++i) peak = fmaxf(peak, p[i]);
+        peak = lanes_peak<LANES>(peak);
         const float from = peak == -INFINITY ? 0.0f : peak;
+        float s = 0.0f;
 #pragma unroll
-        for (int i = 0; i < PER_LANE; ++i) {
-            p[i] = p[i] == -INFINITY ? 0.0f : expf(p[i] - from);
+        for (int i = 0; i < PER; ++i) {
+            p[i] = exp_down(p[i] - from);
             s += p[i];
         }
-        sum = wave_sum(s);
+        sum = lanes_sum<LANES>(s);
     }
 };
+template <DType DT, int PER>
+__device__ __forceinline__ void load_logits(const void* logits, int64_t row, int e0, int E, bool wide,
+                                            float (&p)[PER]) {
+    typedef typename Of<DT>::tag T;
+    load_some<T, PER>((const typename T::type*)logits + row + e0, E - e0, wide, -INFINITY, p);
+}
+
+// Whether rows of PER-element pieces start on 16 bytes.
+inline bool wide_rows(const void* p, int64_t stride, DType dt) {
+    return (uintptr_t)p % 16 == 0 && stride * (dt == kF32 ? 4 : 2) % 16 == 0;
+}
 
 // ------------------------------------------------------------------- balance
 //
 // loss = E sum_e (c_e / C) (S_e / T'): c_e the choices of expert e, C their sum, S_e the sum of
-// the tokens' softmax at e, T' the tokens that may use an expert.  A wave adds a token at a time
-// to its lanes' sums; blocks leave theirs to a second launch, which adds them in order.
-constexpr int kBalanceWaves = 4;
-constexpr int kBalanceThreads = kBalanceWaves * kWave;
-constexpr int kMaxBalanceBlocks = 512;
+// the tokens' softmax at e, T' the tokens that may use an expert.  Lanes add their tokens' shares;
+// blocks leave sums [block][E] and counts [block][E + 1] to a second launch, which adds them in
+// order: the result does not depend on scheduling.
+constexpr int kBalanceThreads = 512;
+constexpr int kMaxBalanceBlocks = 256;
 
-struct BalancePart {            // of a block: sums fp32 [E], counts int32 [E + 1]
+struct BalancePart {
     float* sums;
     int* counts;
 };
-__host__ __device__ inline BalancePart balance_part(void* part, int64_t block, int E) {
-    char* at = (char*)part + block * (2 * (int64_t)E + 1) * 4;
-    return {(float*)at, (int*)(at + 4 * (int64_t)E)};
+__host__ __device__ inline BalancePart balance_part(void* part, int64_t blocks, int64_t block, int E) {
+    return {(float*)part + block * E, (int*)part + blocks * E + block * (E + 1)};
 }
 
-template <DType DT, int PER_LANE>
-__global__ __launch_bounds__(kBalanceThreads) void balance_kernel(const void* logits, int T, int E,
-                                                                  int64_t stride, const int* ids,
-                                                                  int k, void* part) {
-    __shared__ int hist[kWave * PER_LANE];
-    __shared__ float sums[kBalanceWaves][kWave * PER_LANE];
-    __shared__ int used[kBalanceWaves];
-    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-    for (int e = threadIdx.x; e < kWave * PER_LANE; e += kBalanceThreads) hist[e] = 0;
+// The loss of a block's sums: thread e has expert e's choices c and sum s (0 from E on).
+template <int THREADS>
+__device__ __forceinline__ void write_loss(float s, int c, int tokens, int E, float* loss) {
+    __shared__ float product[THREADS / kWave];
+    __shared__ int chosen[THREADS / kWave];
+    float p = wave_sum((float)c * s);
+#pragma unroll
+    for (int d = 1; d < kWave; d <<= 1) c += __shfl_xor(c, d);
+    if (threadIdx.x % kWave == 0) product[threadIdx.x / kWave] = p, chosen[threadIdx.x / kWave] = c;
     __syncthreads();
-    float sum[PER_LANE] = {};
+    if (threadIdx.x != 0) return;
+    for (int w = 1; w < THREADS / kWave; ++w) p += product[w], c += chosen[w];
+    *loss = p * ((float)E / (fmaxf((float)c, 1.0f) * fmaxf((float)tokens, 1.0f)));
+}
+
+// loss: written by this kernel where one block has all tokens (E <= kBalanceThreads), else NULL.
+template <DType DT, int LANES, int PER>
+__global__ __launch_bounds__(kBalanceThreads) void balance_kernel(const void* logits, int T, int E,
+                                                                  int64_t stride, bool wide,
+                                                                  const int* ids, int k, void* part,
+                                                                  float* loss, int* counts) {
+    constexpr int kGroups = kBalanceThreads / LANES, kExperts = LANES * PER;
+    // Sums of a wave's tokens meet in registers first: one row a wave.
+    constexpr int kRows = kBalanceThreads / kWave;
+    __shared__ int hist[kExperts];
+    __shared__ float sums[kRows][kExperts];
+    __shared__ int used;
+    const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES, e0 = lane * PER;
+    for (int e = threadIdx.x; e < kExperts; e += kBalanceThreads) hist[e] = 0;
+    if (threadIdx.x == 0) used = 0;
+    __syncthreads();
+    float sum[PER] = {}, next[PER];
     int tokens = 0;
-    for (int t = blockIdx.x * kBalanceWaves + wave; t < T; t += gridDim.x * kBalanceWaves) {
-        Softmax<DT, PER_LANE> s;
-        s.read(logits, t * stride, E);
-        const int id = lane < k ? ids[(int64_t)t * k + lane] : -1;
-        if (id >= 0 && id < E) atomicAdd(&hist[id], 1);
+    const int64_t step = (int64_t)gridDim.x * kGroups;
+    int64_t t = (int64_t)blockIdx.x * kGroups + group;
+    if (t < T) load_logits<DT>(logits, t * stride, e0, E, wide, next);
+    for (; t < T; t += step) {
+        Softmax<LANES, PER> s;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) s.p[i] = next[i];
+        if (t + step < T) load_logits<DT>(logits, (t + step) * stride, e0, E, wide, next);
+        for (int j = lane; j < k; j += LANES) {
+            const int id = ids[t * k + j];
+            if (id >= 0 && id < E) atomicAdd(&hist[id], 1);
+        }
+        s.make();
         if (s.sum == 0.0f) continue;
         ++tokens;
         const float inv = 1.0f / s.sum;
 #pragma unroll
-        for (int i = 0; i < PER_LANE; ++i) sum[i] += s.p[i] * inv;
+        for (int i = 0; i < PER; ++i) sum[i] += s.p[i] * inv;
     }
+    if (lane == 0) atomicAdd(&used, tokens);
+    // The groups of a wave, then the waves in order.
 #pragma unroll
-    for (int i = 0; i < PER_LANE; ++i) sums[wave][lane + kWave * i] = sum[i];
-    if (lane == 0) used[wave] = tokens;
+    for (int d = LANES; d < kWave; d <<= 1)
+#pragma unroll
+        for (int i = 0; i < PER; ++i) sum[i] += __shfl_xor(sum[i], d);
+    if (threadIdx.x % kWave < LANES) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) sums[threadIdx.x / kWave][e0 + i] = sum[i];
+    }
     __syncthreads();
-    const BalancePart out = balance_part(part, blockIdx.x, E);
-    for (int e = threadIdx.x; e < E; e += kBalanceThreads) {
-        float s = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kBalanceWaves; ++w) s += sums[w][e];
-        out.sums[e] = s;
-        out.counts[e] = hist[e];
-    }
-    if (threadIdx.x == 0) {
-        int n = 0;
-#pragma unroll
-        for (int w = 0; w < kBalanceWaves; ++w) n += used[w];
-        out.counts[E] = n;
-    }
-}
-
-// One block: the blocks' sums in order, then the loss over the experts in order.
-__global__ __launch_bounds__(1024) void balance_sum_kernel(void* part, int blocks, int E,
-                                                           float* loss, int* counts) {
-    __shared__ float product[1024];
-    __shared__ int chosen[1024];
-    __shared__ int tokens;
-    const int e = threadIdx.x;
+    const BalancePart out = balance_part(part, gridDim.x, blockIdx.x, E);
     float s = 0.0f;
     int c = 0;
+    for (int e = threadIdx.x; e < E; e += kBalanceThreads) {
+        s = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kRows; ++w) s += sums[w][e];
+        c = hist[e];
+        if (loss != nullptr) counts[e] = c;
+        else out.sums[e] = s, out.counts[e] = c;
+    }
+    if (threadIdx.x == 0) *(loss != nullptr ? counts + E : out.counts + E) = used;
+    if (loss != nullptr) write_loss<kBalanceThreads>(s, c, used, E, loss);
+}
+
+// One block: every expert's sums over the blocks, rows of them to each of 1024 / experts threads,
+// then the loss.
+__global__ __launch_bounds__(1024) void balance_sum_kernel(void* part, int blocks, int E, int log2_experts,
+                                                           float* loss, int* counts) {
+    __shared__ float sums[1024];
+    __shared__ int chosen[1024];
+    __shared__ int tokens[16];
+    const int tid = threadIdx.x, experts = 1 << log2_experts;
+    const int e = tid & (experts - 1), row = tid >> log2_experts, rows = 1024 >> log2_experts;
+    float s = 0.0f;
+    int c = 0, n = 0;
+    const BalancePart p = balance_part(part, blocks, 0, E);
     if (e < E) {
-        for (int b = 0; b < blocks; ++b) {
-            const BalancePart p = balance_part(part, b, E);
-            s += p.sums[e];
-            c += p.counts[e];
+#pragma unroll 8
+        for (int b = row; b < blocks; b += rows) {
+            s += p.sums[(int64_t)b * E + e];
+            c += p.counts[(int64_t)b * (E + 1) + e];
         }
-        counts[e] = c;
     }
-    if (e == 0) {
-        int n = 0;
-        for (int b = 0; b < blocks; ++b) n += balance_part(part, b, E).counts[E];
-        tokens = n;
-        counts[E] = n;
-    }
-    product[e] = (float)c * s;
-    chosen[e] = c;
+    static_assert(kMaxBalanceBlocks <= 1024, "a thread a block");
+    if (tid < blocks) n = p.counts[(int64_t)tid * (E + 1) + E];
+#pragma unroll
+    for (int d = 1; d < kWave; d <<= 1) n += __shfl_xor(n, d);
+    if (tid % kWave == 0) tokens[tid / kWave] = n;
+    sums[tid] = s;
+    chosen[tid] = c;
     __syncthreads();
-    for (int d = 512; d > 0; d >>= 1) {
-        if (e < d) {
-            product[e] += product[e + d];
-            chosen[e] += chosen[e + d];
-        }
-        __syncthreads();
+    n = 0;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) n += tokens[w];
+    for (int r = 1; r < min(rows, blocks); ++r) {
+        s += sums[(r * experts + tid) & 1023];              // of threads of row 0, the others' are not used
+        c += chosen[(r * experts + tid) & 1023];
     }
-    if (e == 0) {
-        const float scale = (float)E / (fmaxf((float)chosen[0], 1.0f) * fmaxf((float)tokens, 1.0f));
-        *loss = product[0] * scale;
-    }
+    const bool mine = row == 0 && e < E;
+    if (mine) counts[e] = c;
+    if (tid == 0) counts[E] = n;
+    write_loss<1024>(mine ? s : 0.0f, mine ? c : 0, n, E, loss);
 }
 
 // ------------------------------------------------------------- router's gradient
 //
-// A wave per token.  With P the softmax over the usable experts, the loss gives
+// With P the softmax over the usable experts, the loss gives
 //     dloss E / (C T') P_e (c_e - sum_i c_i P_i)
 // and the routing weights, renormalized over the chosen j (w their softmax),
 //     w_j (dw_j - sum_i w_i dw_i) at expert id_j,
 // or not renormalized
 //     P_e (sum of dw_j over the j with id_j = e, less sum_i P_(id_i) dw_i).
-template <DType DT, int PER_LANE>
-__global__ __launch_bounds__(256) void route_grad_kernel(RouteGradArgs a) {
+template <DType DT, int LANES, int PER>
+__global__ __launch_bounds__(256) void route_grad_kernel(RouteGradArgs a, bool wide, bool wide_out) {
     typedef typename Of<DT>::tag T;
-    const int lane = threadIdx.x & (kWave - 1);
-    const int t = blockIdx.x * 4 + threadIdx.x / kWave;
-    if (t >= a.T) return;
-    const int E = a.E;
-    Softmax<DT, PER_LANE> s;
-    s.read(a.logits, t * a.stride, E);
-    const float inv = s.sum == 0.0f ? 0.0f : 1.0f / s.sum;
-    float grad[PER_LANE];
+    constexpr int kSlots = LANES >= 32 ? 1 : 32 / LANES;    // choices of a lane
+    __shared__ __align__(16) float turn[256 / LANES][LANES * PER];
+    const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES, e0 = lane * PER, E = a.E;
+    const int64_t t = (int64_t)blockIdx.x * (256 / LANES) + group;
+    if (t >= a.T) return;                                   // all of a token's lanes
+    Softmax<LANES, PER> s;
+    load_logits<DT>(a.logits, t * a.stride, e0, E, wide, s.p);
+    // Lane j % LANES holds choice j in slot j / LANES.
+    const bool routed = a.dweights != nullptr;
+    int id[kSlots];
+    float l[kSlots], dw[kSlots];
 #pragma unroll
-    for (int i = 0; i < PER_LANE; ++i) {
+    for (int i = 0; i < kSlots; ++i) {
+        const int j = lane + LANES * i;
+        id[i] = -1, l[i] = -INFINITY, dw[i] = 0.0f;
+        if (routed && j < a.k) {
+            id[i] = a.ids[t * a.k + j];
+            dw[i] = a.dweights[t * a.k + j];
+        }
+        if (id[i] < 0 || id[i] >= E) id[i] = -1;
+        else l[i] = T::load(((const typename T::type*)a.logits)[t * a.stride + id[i]]);
+        if (l[i] == -INFINITY) id[i] = -1;                  // an expert that cannot be used
+    }
+    s.make();
+    const float inv = s.sum == 0.0f ? 0.0f : 1.0f / s.sum;
+    float grad[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
         s.p[i] *= inv;
         grad[i] = 0.0f;
     }
     if (a.counts != nullptr) {
-        float c[PER_LANE], all = 0.0f, mean = 0.0f;
+        float c[PER], all = 0.0f, mean = 0.0f;
 #pragma unroll
-        for (int i = 0; i < PER_LANE; ++i) {
-            const int e = lane + kWave * i;
-            c[i] = e < E ? (float)a.counts[e] : 0.0f;
+        for (int i = 0; i < PER; ++i) {
+            c[i] = e0 + i < E ? (float)a.counts[e0 + i] : 0.0f;
             all += c[i];
             mean += c[i] * s.p[i];
         }
-        all = wave_sum(all);
-        mean = wave_sum(mean);
+        all = lanes_sum<LANES>(all);
+        mean = lanes_sum<LANES>(mean);
         const float tokens = fmaxf((float)a.counts[E], 1.0f);
         const float scale = *a.dloss * ((float)E / (fmaxf(all, 1.0f) * tokens));
 #pragma unroll
-        for (int i = 0; i < PER_LANE; ++i) grad[i] = scale * s.p[i] * (c[i] - mean);
+        for (int i = 0; i < PER; ++i) grad[i] = scale * s.p[i] * (c[i] - mean);
     }
-    if (a.dweights != nullptr) {
-        // Lane j < k: choice j.
-        int id = -1;
-        float l = -INFINITY, dw = 0.0f;
-        if (lane < a.k) {
-            id = a.ids[(int64_t)t * a.k + lane];
-            if (id < 0 || id >= E) id = -1;
-            else l = load<DT>(a.logits, t * a.stride + id);
-            if (id >= 0) dw = a.dweights[(int64_t)t * a.k + lane];
-        }
-        if (l == -INFINITY) id = -1, dw = 0.0f;         // an expert that cannot be used
-        float w = 0.0f;
+    if (routed) {
+        float peak = s.peak, sum = 0.0f, mean = 0.0f, w[kSlots];
         if (a.renormalize) {
-            const float peak = wave_peak(l);
-            if (id >= 0) w = expf(l - peak);
-            const float sum = wave_sum(w);
-            if (id >= 0) w /= sum;
-        } else if (id >= 0) {
-            w = expf(l - s.peak) * inv;
+            peak = l[0];
+#pragma unroll
+            for (int i = 1; i < kSlots; ++i) peak = fmaxf(peak, l[i]);
+            peak = lanes_peak<LANES>(peak);
         }
-        const float mean = wave_sum(w * dw);
-        const float mine = a.renormalize ? w * (dw - mean) : w * dw;
+#pragma unroll
+        for (int i = 0; i < kSlots; ++i) {
+            w[i] = id[i] >= 0 ? exp_down(l[i] - peak) : 0.0f;
+            sum += w[i];
+        }
+        const float per = a.renormalize ? 1.0f / lanes_sum<LANES>(sum) : inv;
+#pragma unroll
+        for (int i = 0; i < kSlots; ++i) {
+            w[i] = id[i] >= 0 ? w[i] * per : 0.0f;
+            mean += id[i] >= 0 ? w[i] * dw[i] : 0.0f;
+        }
+        mean = lanes_sum<LANES>(mean);
         if (!a.renormalize) {
 #pragma unroll
-            for (int i = 0; i < PER_LANE; ++i) grad[i] -= s.p[i] * mean;
+            for (int i = 0; i < PER; ++i) grad[i] -= s.p[i] * mean;
         }
-        for (int j = 0; j < a.k; ++j) {
-            const int e = __builtin_amdgcn_readlane(id, j);
-            const float v = __builtin_bit_cast(
-                float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, mine), j));
+        // To the experts' lanes through LDS (the wave's own part of it).  Where a token names an
+        // expert twice, a choice does not find its own number again: then one by one.
+        float* mark = turn[group];
+        auto settle = [] {
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+        };
+        bool twice = false;
 #pragma unroll
-            for (int i = 0; i < PER_LANE; ++i)
-                if (e == lane + kWave * i) grad[i] += v;
+        for (int i = 0; i < kSlots; ++i)
+            if (id[i] >= 0) mark[id[i]] = (float)(lane + LANES * i);
+        settle();
+#pragma unroll
+        for (int i = 0; i < kSlots; ++i)
+            if (id[i] >= 0) twice = twice || mark[id[i]] != (float)(lane + LANES * i);
+        settle();
+        float add[PER];
+#pragma unroll
+        for (int i = 0; i < PER; ++i) turn[group][e0 + i] = 0.0f;
+        settle();
+        const bool one_by_one = __any(twice);
+#pragma unroll
+        for (int i = 0; i < kSlots; ++i) {
+            const float mine = a.renormalize ? w[i] * (dw[i] - mean) : w[i] * dw[i];
+            if (!one_by_one) {
+                if (id[i] >= 0) turn[group][id[i]] = mine;
+            } else {
+                for (int j = 0; j < LANES; ++j) {
+                    if (lane == j && id[i] >= 0) turn[group][id[i]] += mine;
+                    settle();
+                }
+            }
         }
+        settle();
+#pragma unroll
+        for (int i = 0; i < PER; ++i) add[i] = turn[group][e0 + i];
+#pragma unroll
+        for (int i = 0; i < PER; ++i) grad[i] += add[i];
     }
-    typename T::type* out = (typename T::type*)a.dlogits + (int64_t)t * E;
+    typename T::type* out = (typename T::type*)a.dlogits + t * E + e0;
+    typename T::type o[PER];
 #pragma unroll
-    for (int i = 0; i < PER_LANE; ++i) {
-        const int e = lane + kWave * i;
-        if (e < E) out[e] = T::store(grad[i]);
+    for (int i = 0; i < PER; ++i) o[i] = T::store(grad[i]);
+    if (wide_out && e0 + PER <= E) {
+        __builtin_memcpy(__builtin_assume_aligned(out, 16), o, sizeof(o));
+    } else {
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            if (e0 + i < E) out[i] = o[i];
     }
 }
 
@@ -281,22 +407,29 @@ __global__ __launch_bounds__(256) void combine_grad_kernel(const uint16_t* dout,
                 const uint64_t named = __ballot(same);
                 const bool write = tokens[r] == t && __builtin_ctzll(named) == j;
                 const float w = wave_sum(same ? weights[(int64_t)t * k + lane] : 0.0f);
-                for (int n = lane * VEC; n < N; n += kWave * VEC) {
-                    uint16_t d[VEC], o[VEC];
-                    typename ROW::type y[VEC];
-                    constexpr int kAlign = sizeof(y) < 16 ? sizeof(y) : 16;
-                    __builtin_memcpy(d, __builtin_assume_aligned(dout + (int64_t)t * N + n, 2 * VEC),
-                                     sizeof(d));
-                    __builtin_memcpy(y, __builtin_assume_aligned(Y + (int64_t)r * N + n, kAlign),
-                                     sizeof(y));
+                constexpr int kHand = VEC == 8 ? 4 : 1;     // pieces of the rows in hand
+                for (int n0 = lane * VEC; n0 < N; n0 += kHand * kWave * VEC) {
+                    Piece<uint16_t, VEC> d[kHand], o;
+                    Piece<typename ROW::type, VEC> y[kHand];
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i) {
-                        dot = fmaf(T::load(d[i]), ROW::load(y[i]), dot);
-                        o[i] = T::store(w * T::load(d[i]));
+                    for (int h = 0; h < kHand; ++h) {
+                        const int n = n0 + h * kWave * VEC;
+                        if (n >= N) continue;
+                        d[h].load(dout + (int64_t)t * N + n);
+                        y[h].load_once(Y + (int64_t)r * N + n);
                     }
-                    if (write)
-                        __builtin_memcpy(__builtin_assume_aligned(dY + (int64_t)r * N + n, 2 * VEC),
-                                         o, sizeof(o));
+#pragma unroll
+                    for (int h = 0; h < kHand; ++h) {
+                        const int n = n0 + h * kWave * VEC;
+                        if (n >= N) continue;
+#pragma unroll
+                        for (int i = 0; i < VEC; ++i) {
+                            const float e = T::load(d[h].get(i));
+                            dot = fmaf(e, ROW::load(y[h].get(i)), dot);
+                            o.set(i, T::store(w * e));
+                        }
+                        if (write) o.store_once(dY + (int64_t)r * N + n);
+                    }
                 }
                 dot = wave_sum(dot);
             }
@@ -307,9 +440,10 @@ __global__ __launch_bounds__(256) void combine_grad_kernel(const uint16_t* dout,
             const bool named = t >= 0 && t < T_ &&
                                __any(lane < k && positions[(int64_t)t * k + lane] == (int)c);
             if (!named) {
-                const uint16_t o[VEC] = {};
-                for (int n = lane * VEC; n < N; n += kWave * VEC)
-                    __builtin_memcpy(__builtin_assume_aligned(dY + c * N + n, 2 * VEC), o, sizeof(o));
+                Piece<uint16_t, VEC> o;
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) o.set(i, 0);
+                for (int n = lane * VEC; n < N; n += kWave * VEC) o.store_once(dY + c * N + n);
             }
         }
     }
@@ -330,13 +464,18 @@ void combine_grad(const uint16_t* dout, const void* Y, int R, int N, const int* 
                                                                  weights, T_, k, dY, dweights);
 }
 
-// Experts a lane holds.
+// Lanes of a token and experts of a lane.
+template <int LANES, int PER>
+struct Lanes {
+    static constexpr int lanes = LANES, per = PER;
+};
 template <class F>
 void by_experts(int E, F f) {
-    if (E <= 64) f(std::integral_constant<int, 1>());
-    else if (E <= 128) f(std::integral_constant<int, 2>());
-    else if (E <= 256) f(std::integral_constant<int, 4>());
-    else f(std::integral_constant<int, 16>());
+    if (E <= 64) f(Lanes<8, 8>());
+    else if (E <= 128) f(Lanes<16, 8>());
+    else if (E <= 256) f(Lanes<32, 8>());
+    else if (E <= 512) f(Lanes<64, 8>());
+    else f(Lanes<64, 16>());
 }
 template <class F>
 void by_dtype(DType dt, F f) {
@@ -345,40 +484,53 @@ void by_dtype(DType dt, F f) {
     else f(std::integral_constant<DType, kF32>());
 }
 
-int balance_blocks(int64_t T) {
-    const int64_t blocks = (T + kBalanceWaves - 1) / kBalanceWaves;
+// Blocks of at least two tokens a group of lanes.
+int balance_blocks(int64_t T, int E) {
+    int lanes = 8;
+    by_experts(E, [&](auto n) { lanes = decltype(n)::lanes; });
+    const int64_t each = 2 * (kBalanceThreads / lanes), blocks = (T + each - 1) / each;
     return (int)(blocks < kMaxBalanceBlocks ? blocks : kMaxBalanceBlocks);
 }
 
 }  // namespace
 
 size_t balance_workspace(int64_t T, int64_t E) {
-    return (size_t)balance_blocks(T) * (2 * E + 1) * 4;
+    const int blocks = balance_blocks(T, (int)E);
+    return blocks == 1 && E <= kBalanceThreads ? 0 : (size_t)blocks * (2 * E + 1) * 4;
 }
 
 hipError_t launch_balance(const void* logits, DType dt, int T, int E, int64_t stride,
                           const int* ids, int k, float* loss, int* counts, void* part,
                           hipStream_t stream) {
-    const int blocks = balance_blocks(T);
+    const int blocks = balance_blocks(T, E);
+    const bool wide = wide_rows(logits, stride, dt), one = blocks == 1 && E <= kBalanceThreads;
     if (blocks > 0) {
         by_dtype(dt, [&](auto d) {
             by_experts(E, [&](auto n) {
-                balance_kernel<decltype(d)::value, decltype(n)::value>
-                    <<<blocks, kBalanceThreads, 0, stream>>>(logits, T, E, stride, ids, k, part);
+                typedef decltype(n) L;
+                balance_kernel<decltype(d)::value, L::lanes, L::per>
+                    <<<blocks, kBalanceThreads, 0, stream>>>(logits, T, E, stride, wide, ids, k, part,
+                                                             one ? loss : nullptr, counts);
             });
         });
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    balance_sum_kernel<<<1, 1024, 0, stream>>>(part, blocks, E, loss, counts);
+    if (one) return hipSuccess;
+    int log2_experts = 0;
+    while (1 << log2_experts < E) ++log2_experts;
+    balance_sum_kernel<<<1, 1024, 0, stream>>>(part, blocks, E, log2_experts, loss, counts);
     return hipGetLastError();
 }
 
 hipError_t launch_route_grad(const RouteGradArgs& a, DType dt, hipStream_t stream) {
-    const unsigned grid = (unsigned)((a.T + 3) / 4);
+    const bool wide = wide_rows(a.logits, a.stride, dt), wide_out = wide_rows(a.dlogits, a.E, dt);
     by_dtype(dt, [&](auto d) {
         by_experts(a.E, [&](auto n) {
-            route_grad_kernel<decltype(d)::value, decltype(n)::value><<<grid, 256, 0, stream>>>(a);
+            typedef decltype(n) L;
+            constexpr int kTokens = 256 / L::lanes;
+            route_grad_kernel<decltype(d)::value, L::lanes, L::per>
+                <<<(unsigned)((a.T + kTokens - 1) / kTokens), 256, 0, stream>>>(a, wide, wide_out);
         });
     });
     return hipGetLastError();

@@ -118,6 +118,43 @@ __device__ __forceinline__ void split_bf16(half8_t x, bf168_t& hi, bf168_t& lo) 
     }
 }
 
+// N neighbouring elements of a row that starts on 16 bytes (N = 8) or on an element (N = 1), moved
+// as they are.  _once: memory that no one reads again soon stays out of the caches.
+template <typename E, int N>
+struct Piece {
+    static constexpr int kBytes = sizeof(E) * N, kWords = kBytes / 16;
+    union {
+        E e[N];
+        uint4_t q[kWords > 0 ? kWords : 1];
+    };
+    __device__ __forceinline__ void load(const E* p) {
+        if constexpr (kWords > 0) {
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) q[i] = ((const uint4_t*)p)[i];
+        } else {
+            e[0] = *p;
+        }
+    }
+    __device__ __forceinline__ void load_once(const E* p) {
+        if constexpr (kWords > 0) {
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) q[i] = __builtin_nontemporal_load((const uint4_t*)p + i);
+        } else {
+            e[0] = *p;
+        }
+    }
+    __device__ __forceinline__ void store_once(E* p) const {
+        if constexpr (kWords > 0) {
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) __builtin_nontemporal_store(q[i], (uint4_t*)p + i);
+        } else {
+            *p = e[0];
+        }
+    }
+    __device__ __forceinline__ E get(int i) const { return e[i]; }
+    __device__ __forceinline__ void set(int i, E v) { e[i] = v; }
+};
+
 // Largest value over the lanes l ^ 1 and l ^ 2 (groups of four lanes).
 __device__ __forceinline__ uint32_t quad_max(uint32_t v) {
     const uint32_t a = __builtin_amdgcn_update_dpp(0, v, 0xB1, 0xF, 0xF, true);   // [1,0,3,2]
