@@ -192,7 +192,8 @@ enum {
  *   Y        out: [M, F] of X's dtype, dense
  *   Z        out: [M, N] of X's dtype, dense: z, for the backward pass; or NULL
  * Sums, z and the activation are fp32; Y and Z are rounded once each.
- * workspace as for mxfp4_linear (mxfp4_linear_workspace_bytes). */
+ * workspace as for mxfp4_linear, with its own size. */
+size_t mxfp4_linear_act_workspace_bytes(int64_t M, int64_t N, int64_t K);
 int mxfp4_linear_act(const void* X, int dtype, int64_t M, int64_t x_stride, const uint8_t* codes,
                      const uint8_t* scales, int64_t N, int64_t K, const void* bias,
                      int activation, const void* residual, int64_t r_stride, void* Y, void* Z,

@@ -57,13 +57,16 @@ def slope(z, act):
 
 def act_bound(z, act, y):
     """Error of the activation's own fp32 arithmetic: the argument of an exponential carries
-    its relative rounding (2^-23 of it and of what is derived from it) into the result."""
+    its relative rounding (2^-23 of it and of what is derived from it) into the result.  A factor
+    below fp32's normal range, 2^-126, may count as 0: a sigmoid is that small where |z| > 87.3, and
+    |z| times a smaller one falls from there on, 87.4 * 2^-126 < 2^-119 (erfc and the tanh form
+    reach it where |z| < 14)."""
     with np.errstate(all="ignore"):
         a = np.abs(z)
         arg = {"none": 0 * a, "relu": 0 * a, "silu": a, "gelu": a * a,
                "gelu_tanh": C * (a + 0.05 * a ** 3)}[act]
         own = (arg + 16) * 2.0 ** -22 * np.abs(y) if act not in ("none", "relu") else 0 * a
-        return np.where(np.isfinite(own), own, 0) + 2.0 ** -120
+        return np.where(np.isfinite(own), own, 0) + 2.0 ** -119
 
 
 # Largest slopes: silu 1.0999, gelu and its tanh form 1.129.

@@ -53,7 +53,7 @@ def test_linear_act_valid_calls(lib):  # noqa: F811
     # with SwiGLU Y is half of Z's width
     assert call(act=SWIGLU, rs=4, Y=F - 32) == DEVICE and call(Y=F - 32) == INVALID
     M, N, K = 50, 512, 8192
-    need = lib.mxfp4_linear_workspace_bytes(M, N, K)
+    need = lib.mxfp4_linear_act_workspace_bytes(M, N, K)
     assert need > 0
     far = 16 * FAKE
 

@@ -32,7 +32,7 @@ __global__ __launch_bounds__(256) void finish_kernel(LinearArgs a) {
                 for (int j = 0; j < VEC; ++j) up[j] += v[j];
             }
         }
-        finish_columns<T, VEC>(a, 0, row, col, h, up);
+        finish_columns<T, VEC>(a, load_bias<T, VEC>(a, 0, col), row, col, h, up);
     }
 }
 
@@ -80,22 +80,29 @@ __global__ __launch_bounds__(kThreads) void act_grad_kernel(ActGradArgs a) {
                 const int64_t row = t.row0 + r0 + h * kRowLanes;
                 if (r0 + h * kRowLanes >= t.rows) continue;
                 Piece<uint16_t, VEC> out[H];
+                float dz[H][VEC], g[VEC];
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) {
-                    const float d = T::load(dy[h].get(j)), g = T::load(z[h].get(j));
-                    float dz[H];
-                    if constexpr (SWIGLU) {
-                        dz[0] = d * T::load(up[h].get(j)) * silu_slope(g);
-                        dz[1] = d * silu(g);
-                    } else {
-                        dz[0] = d * act_slope(a.act, g);
-                    }
+                for (int j = 0; j < VEC; ++j) g[j] = T::load(z[h].get(j));
+                if constexpr (SWIGLU) {
 #pragma unroll
-                    for (int i = 0; i < H; ++i) {
-                        out[i].set(j, T::store(dz[i]));
-                        sum[i][j] += dz[i];
+                    for (int j = 0; j < VEC; ++j) {
+                        const float d = T::load(dy[h].get(j)), u = T::load(up[h].get(j));
+                        const float s = sigmoid(g[j]), c = clamp_to(g[j], 150.0f);
+                        dz[0][j] = d * u * silu_slope(c, s);
+                        dz[1][j] = d * (g[j] * s);
                     }
+                } else {
+                    act_slopes(a.act, g);
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) dz[0][j] = T::load(dy[h].get(j)) * g[j];
                 }
+#pragma unroll
+                for (int i = 0; i < H; ++i)
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) {
+                        out[i].set(j, T::store(dz[i][j]));
+                        sum[i][j] += dz[i][j];
+                    }
 #pragma unroll
                 for (int i = 0; i < H; ++i) out[i].store_once(a.dZ + row * a.N + i * F + col);
             }

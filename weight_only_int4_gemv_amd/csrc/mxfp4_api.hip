@@ -316,6 +316,11 @@ int moe_combine(const void* Y, int dtype, int64_t R, int64_t N, const int32_t* p
                                            stream_of(stream)));
 }
 
+size_t mxfp4_linear_act_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+    if (bad_size(M) || bad_size(N) || check_k(K)) return 0;
+    return mxfp4::linear_act_workspace(M, N, K);
+}
+
 int mxfp4_linear_act(const void* X, int dtype, int64_t M, int64_t x_stride, const uint8_t* codes,
                      const uint8_t* scales, int64_t N, int64_t K, const void* bias,
                      int activation, const void* residual, int64_t r_stride, void* Y, void* Z,
@@ -333,7 +338,7 @@ int mxfp4_linear_act(const void* X, int dtype, int64_t M, int64_t x_stride, cons
     if (!aligned(X, 16) || !aligned(codes, 16) || !aligned(Y, 2) || !aligned(Z, 2) ||
         !aligned(bias, 2) || !aligned(residual, 2) || (M > 1 && x_stride % 8))
         return W4A16_ERR_MISALIGNED;
-    const size_t need = mxfp4_linear_workspace_bytes(M, N, K);
+    const size_t need = mxfp4_linear_act_workspace_bytes(M, N, K);
     if (const int st = check_workspace(workspace, workspace_bytes, need, 16)) return st;
     const Span out[] = {{Y, (uint64_t)M * F * 2}, {Z, (uint64_t)M * N * 2}, {workspace, need}};
     const Span in[] = {{X, span_bytes(M, K, x_stride, 2)},

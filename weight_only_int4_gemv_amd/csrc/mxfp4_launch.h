@@ -54,7 +54,8 @@ constexpr int64_t kMaxGrid = (int64_t)1 << 22;      // blocks of a launch (threa
 // linear_workspace bytes for the partial sums of K slices, or NULL for no split.
 size_t linear_workspace(int64_t M, int64_t N, int64_t K);
 hipError_t launch_linear(LinearArgs a, DType dt, float* part, hipStream_t stream);
-// The same with the epilogue.
+// The same with the epilogue; dense with its own size of part.
+size_t linear_act_workspace(int64_t M, int64_t N, int64_t K);
 hipError_t launch_linear_act(LinearArgs a, DType dt, float* part, hipStream_t stream);
 // Few rows per weight matrix: weights straight into matrix-core registers.
 hipError_t launch_stream(const LinearArgs& a, DType dt, hipStream_t stream);

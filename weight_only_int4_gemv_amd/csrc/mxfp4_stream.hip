@@ -189,7 +189,7 @@ __global__ __launch_bounds__(kWaves* kWave) void stream_kernel(LinearArgs a) {
         }
         if constexpr (EPILOGUE) {
             const float z[1] = {h[0]}, up[1] = {h[1]};
-            finish_columns<T, 1>(a, t.expert, t.row0 + r, col0 + n, z, up);
+            finish_columns<T, 1>(a, load_bias<T, 1>(a, t.expert, col0 + n), t.row0 + r, col0 + n, z, up);
             continue;
         }
         const float y = a.swiglu ? silu(h[0]) * h[1] : h[0];

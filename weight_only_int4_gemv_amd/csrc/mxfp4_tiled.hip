@@ -398,11 +398,7 @@ __global__ __launch_bounds__(C::kThreads, C::kPerCu * C::kWaves / 4) void tiled_
         if constexpr (EPILOGUE) {
             auto finish = [&](auto vec) {
                 constexpr int VEC = decltype(vec)::value;
-                const int chunks = wcols / VEC;
-#pragma unroll 1
-                for (int i = lane; i < 32 * chunks; i += kWave) {
-                    const int r = i / chunks, c = i % chunks * VEC;
-                    if (r >= rows || c >= cols) continue;
+                auto item = [&](int r, int c, const Bias<VEC>& bias) {
                     const float* from = &turn[r * C::kPitch + c];
                     float h[VEC], up[VEC] = {};
 #pragma unroll
@@ -410,7 +406,21 @@ __global__ __launch_bounds__(C::kThreads, C::kPerCu * C::kWaves / 4) void tiled_
                         h[j] = from[j];
                         if (NT > 1 && a.swiglu) up[j] = from[32 + j];
                     }
-                    finish_columns<T, VEC>(a, t.expert, t.row0 + 32 * m + r, wcol0 + c, h, up);
+                    finish_columns<T, VEC>(a, bias, t.row0 + 32 * m + r, wcol0 + c, h, up);
+                };
+                const int chunks = wcols / VEC;
+                if constexpr (VEC == 8) {                   // a lane's columns are the same in all rows
+                    const int c = lane % chunks * VEC;
+                    if (c >= cols) return;
+                    const Bias<VEC> bias = load_bias<T, VEC>(a, t.expert, wcol0 + c);
+#pragma unroll 2
+                    for (int r = lane / chunks; r < rows; r += kWave / chunks) item(r, c, bias);
+                } else {
+#pragma unroll 1
+                    for (int i = lane; i < 32 * chunks; i += kWave) {
+                        const int r = i / chunks, c = i % chunks;
+                        if (r < rows && c < cols) item(r, c, load_bias<T, VEC>(a, t.expert, wcol0 + c));
+                    }
                 }
             };
             if (finish_wide(a)) finish(Int<8>());
@@ -523,11 +533,45 @@ Choice choose(int64_t R, int64_t E, int64_t N, int64_t K, bool grouped, bool spl
     return c;
 }
 
+// Kernel and K split of a dense product with an epilogue: as above up to 32 rows, else the least of
+// what tilings and slices take.  With 4096 columns a block of Large takes 53 us beside another (64
+// alone), of Medium 31.5 and of Narrow 18.9, and they add up over the blocks of a CU (14336 weight
+// rows, 701 rows: 103 / 98 / 105 us, 300 rows 64 / 62 / 55, 2000 rows 227 / 246 / 283; 4096 x 14336,
+// 701 rows: 129 us unsplit, 102 in 4 slices of Medium).  A second launch adds the slices' sums.
+Choice choose_act(int64_t R, int64_t N, int64_t K, bool split) {
+    Choice best = choose(R, 1, N, K, false, split);
+    if (R <= 32) return best;
+    const int64_t total = (K / kBlock + 1) / 2;
+    double least = 0;
+    for (const Kernel kernel : {kLarge, kMedium, kNarrow}) {
+        const int bm = kernel == kLarge ? 128 : 64, bn = kernel == kNarrow ? 128 : 256;
+        const int64_t tiles = (R + bm - 1) / bm * ((N + bn - 1) / bn);
+        for (int64_t s = 1; s <= (split ? 8 : 1) && (s == 1 || total / s >= 8); ++s) {
+            const int64_t steps = total > 0 ? (total + s - 1) / s : 1, slices = total > 0 ? (total + steps - 1) / steps : 1;
+            const double n = double(tiles * slices) / 256, cus = n > 1 ? (double)(int64_t)(n + 0.999) : 1;
+            double us = kernel == kLarge ? 10 + 53 * cus : kernel == kMedium ? 25 + 31.5 * n : 12 + 18.9 * n;
+            us *= double(steps) / 64;
+            if (slices > 1) us += 5 + double(slices) * R * N * 8 / 8e6;
+            if (least == 0 || us < least) {
+                least = us;
+                best = Choice{kernel, (int)slices, (int)steps};
+            }
+        }
+    }
+    return best;
+}
+
 }  // namespace
 
 size_t linear_workspace(int64_t M, int64_t N, int64_t K) {
     if (M <= 0 || N <= 0) return 0;
     const Choice c = choose(M, 1, N, K, false, true);
+    return c.slices > 1 ? (size_t)c.slices * M * N * sizeof(float) : 0;
+}
+
+size_t linear_act_workspace(int64_t M, int64_t N, int64_t K) {
+    if (M <= 0 || N <= 0) return 0;
+    const Choice c = choose_act(M, N, K, true);
     return c.slices > 1 ? (size_t)c.slices * M * N * sizeof(float) : 0;
 }
 
@@ -549,7 +593,8 @@ hipError_t launch_linear(LinearArgs a, DType dt, float* part, hipStream_t stream
 // Unsplit, the product's own kernel ends with the epilogue; K slices leave their sums to a
 // second launch, which has to read them anyway.
 hipError_t launch_linear_act(LinearArgs a, DType dt, float* part, hipStream_t stream) {
-    Choice c = choose(a.R, a.E, a.N, a.K, a.offsets != nullptr, part != nullptr);
+    Choice c = a.offsets != nullptr ? choose(a.R, a.E, a.N, a.K, true, false)
+                                    : choose_act(a.R, a.N, a.K, part != nullptr);
     a.slices = c.slices, a.steps = c.steps;
     if (c.slices > 1) {
         a.part = part;

@@ -81,7 +81,8 @@ _SIGNATURES = {
     "moe_combine_grad": [_p, _int, _i64, _i64, _p, _i64, _p, _p, _p, _i64, _p, _p, _p],
 }
 _SIZES = ("mxfp4_linear_workspace_bytes", "mxfp4_matmul_workspace_bytes",
-          "moe_plan_workspace_bytes", "mxfp4_activation_grad_workspace_bytes",
+          "moe_plan_workspace_bytes", "mxfp4_linear_act_workspace_bytes",
+          "mxfp4_activation_grad_workspace_bytes",
           "mxfp4_linear_grad_workspace_bytes", "moe_balance_workspace_bytes")
 _lib = None
 
@@ -159,6 +160,8 @@ def _stream(*tensors) -> int:
 
 def _row_stride(t: torch.Tensor, name: str) -> int:
     """Elements between the rows of a 2-d tensor whose rows are dense."""
+    if t.is_contiguous():
+        return t.shape[1]
     rows, cols = t.shape
     if rows and cols > 1 and t.stride(1) != 1:
         raise ValueError("the rows of %s must be dense, got strides %s" % (name, t.stride()))
@@ -460,6 +463,12 @@ def _bias(bias, shape, X: torch.Tensor) -> None:
         raise ValueError("bias has shape %s, want %s" % (tuple(bias.shape), shape))
 
 
+def linear_act_workspace(M: int, N: int, K: int, device="cuda") -> torch.Tensor:
+    """A workspace for linear_act() (uint8, at least 1 byte)."""
+    n = _workspace_bytes("mxfp4_linear_act_workspace_bytes", M, N, K)
+    return torch.empty(max(1, n), dtype=torch.uint8, device=device)
+
+
 def linear_act(X: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
                bias: torch.Tensor = None, activation: str = None, residual: torch.Tensor = None,
                save: bool = False, Y: torch.Tensor = None, Z: torch.Tensor = None,
@@ -469,7 +478,8 @@ def linear_act(X: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
     dtype or None.  activation: one of ACTIVATIONS; swiglu takes weights of gate rows,
     then up rows, F = N / 2, otherwise F = N.  Y [M, F] is of X's dtype; with save (or
     Z given) the result is (Y, Z), Z [M, N] what the activation was applied to.
-    workspace as in linear()."""
+    workspace: from linear_act_workspace(), else allocated per call where the shape uses
+    one."""
     lib = library()
     N, K = _weights(codes, scales, 2)
     _need(X, "X", _HALVES, 2, dense=False)
@@ -490,7 +500,7 @@ def linear_act(X: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
     save = save or Z is not None
     if save:
         Z = _out(Z, (M, N), X.dtype, X, "Z")
-    ws, ws_bytes, keep = _workspace(_workspace_bytes("mxfp4_linear_workspace_bytes", M, N, K),
+    ws, ws_bytes, keep = _workspace(_workspace_bytes("mxfp4_linear_act_workspace_bytes", M, N, K),
                                     workspace, X)
     _check("mxfp4_linear_act",
            lib.mxfp4_linear_act(X.data_ptr(), _HALVES[X.dtype], M, stride, codes.data_ptr(),
