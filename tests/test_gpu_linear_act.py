@@ -78,6 +78,46 @@ def test_linear_act(mx, dtype, act, M, N, K):
 
 
 @pytest.mark.parametrize("dtype", HALVES)
+@pytest.mark.parametrize("act", ["none", "gelu", "swiglu"])
+@pytest.mark.parametrize("N,K", [(4096, 4096), (1198, 14336), (16390, 1056), (66000, 256), (3500, 14976)])
+def test_linear_act_one_row_of_many_weights(mx, dtype, act, N, K):
+    """The kernel along the rows: one to eight waves on a row, ends of rows and of K inside a wave."""
+    say("linear_act one row %s %s N=%d K=%d" % (dtype, act, N, K))
+    check_linear(mx, np.random.default_rng([N, K]), 1, N, K, dtype, act, residual=act == "none")
+
+
+@pytest.mark.parametrize("dtype", HALVES)
+def test_linear_act_one_row_specials(mx, dtype):
+    """Every scale byte, x up to the type's ends, an infinity in the last block."""
+    say("linear_act one row specials %s" % dtype)
+    rng = np.random.default_rng(12)
+    N, K = 8200, 2080
+    for low, high in ((90, 120), (118, 150), (0, 3)):       # above 250 products of N(0, 1) pass fp32
+        check_linear(mx, rng, 1, N, K, dtype, "none", low=low, high=high)
+    codes, scales = weights(rng, (N, K), 60, 70)
+    scales[7, 3], scales[8, 64], scales[9, 0] = 253, 254, 255
+    top, low = (2.0 ** 15, 2.0 ** -24) if dtype == torch.float16 else (2.0 ** 127, 2.0 ** -133)
+    x = rng.standard_normal((1, K))
+    x[0, ::5], x[0, 1::7] = top, low
+    x = gpu(x, dtype)
+    y = mx.linear_act(x, gpu(codes), gpu(scales))
+    w = ref.values(codes, scales)
+    z, mags = ref.product(ref.f64(x), w)
+    # weights of 2^126 and more meet 2^127 here: the sum's parts pass fp32, their sign is the sum's or not
+    far = (scales >= 253).any(axis=1)
+    ref.check(y[:, ~far], z[:, ~far], (ref.sum_bound(K, mags) + ref.rounded(np.abs(z), dtype))[:, ~far], dtype)
+    assert y[0, 9].isnan()
+    x[0, K - 1] = float("inf")
+    y = mx.linear_act(x, gpu(codes), gpu(scales))
+    assert not y.isfinite().any()
+    x = gpu(rng.standard_normal((1, K)) * 2.0 ** -10, dtype)
+    scales[9, 0] = 120
+    z, mags = ref.product(ref.f64(x), ref.values(codes, scales))
+    ref.check(mx.linear_act(x, gpu(codes), gpu(scales)), z,
+              ref.sum_bound(K, mags) + ref.rounded(np.abs(z), dtype), dtype)
+
+
+@pytest.mark.parametrize("dtype", HALVES)
 @pytest.mark.parametrize("M", [5, 50])
 def test_linear_act_strides_and_alignment(mx, dtype, M):
     """Rows of X and of the residual further apart, outputs off 16 bytes."""
@@ -126,7 +166,7 @@ def test_linear_act_slices_and_workspaces(mx, dtype, act):
 
 def test_linear_act_without_anything_is_linear(mx):
     """Bit for bit where both sum in the same order (no other split of K)."""
-    for M in (1, 16, 24):
+    for M in (2, 16, 24):
         rng = np.random.default_rng(M)
         codes, scales = (gpu(t) for t in weights(rng, (512, 1024)))
         x = gpu(rng.standard_normal((M, 1024)), torch.bfloat16)

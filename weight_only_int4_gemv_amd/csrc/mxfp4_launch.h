@@ -60,6 +60,9 @@ hipError_t launch_linear_act(LinearArgs a, DType dt, float* part, hipStream_t st
 // Few rows per weight matrix: weights straight into matrix-core registers.
 hipError_t launch_stream(const LinearArgs& a, DType dt, hipStream_t stream);
 
+// One row with the epilogue, where X fits LDS and the weights are many.
+bool gemv_fits(int64_t R, int64_t N, int64_t K);
+hipError_t launch_gemv(const LinearArgs& a, DType dt, hipStream_t stream);
 // The epilogue of the K slices' partial sums [slices][R][N], added in slice order.
 hipError_t launch_finish(const LinearArgs& a, DType dt, hipStream_t stream);
 

@@ -593,6 +593,7 @@ hipError_t launch_linear(LinearArgs a, DType dt, float* part, hipStream_t stream
 // Unsplit, the product's own kernel ends with the epilogue; K slices leave their sums to a
 // second launch, which has to read them anyway.
 hipError_t launch_linear_act(LinearArgs a, DType dt, float* part, hipStream_t stream) {
+    if (a.offsets == nullptr && gemv_fits(a.R, a.N, a.K)) return launch_gemv(a, dt, stream);
     Choice c = a.offsets != nullptr ? choose(a.R, a.E, a.N, a.K, true, false)
                                     : choose_act(a.R, a.N, a.K, part != nullptr);
     a.slices = c.slices, a.steps = c.steps;
