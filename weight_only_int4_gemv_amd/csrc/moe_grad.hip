@@ -175,7 +175,7 @@ __global__ __launch_bounds__(kBalanceThreads) void balance_kernel(const void* lo
         s.make();
         if (s.sum == 0.0f) continue;
         ++tokens;
-        const float inv = 1.0f / s.sum;
+        const float inv = __builtin_amdgcn_rcpf(s.sum);
 #pragma unroll
         for (int i = 0; i < PER; ++i) sum[i] += s.p[i] * inv;
     }
@@ -247,7 +247,8 @@ __global__ __launch_bounds__(1024) void balance_sum_kernel(void* part, int block
 
 // ------------------------------------------------------------- router's gradient
 //
-// With P the softmax over the usable experts, the loss gives
+// Four waves a SIMD walk over the tokens, the next logits on their way (65521 tokens of 128 experts
+// 14 us; as many waves as tokens need 23).  With P the softmax over the usable experts, the loss gives
 //     dloss E / (C T') P_e (c_e - sum_i c_i P_i)
 // and the routing weights, renormalized over the chosen j (w their softmax),
 //     w_j (dw_j - sum_i w_i dw_i) at expert id_j,
@@ -259,122 +260,138 @@ __global__ __launch_bounds__(256) void route_grad_kernel(RouteGradArgs a, bool w
     constexpr int kSlots = LANES >= 32 ? 1 : 32 / LANES;    // choices of a lane
     __shared__ __align__(16) float turn[256 / LANES][LANES * PER];
     const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES, e0 = lane * PER, E = a.E;
-    const int64_t t = (int64_t)blockIdx.x * (256 / LANES) + group;
+    const int64_t step = (int64_t)gridDim.x * (256 / LANES);
+    int64_t t = (int64_t)blockIdx.x * (256 / LANES) + group;
     if (t >= a.T) return;                                   // all of a token's lanes
-    Softmax<LANES, PER> s;
-    load_logits<DT>(a.logits, t * a.stride, e0, E, wide, s.p);
-    // Lane j % LANES holds choice j in slot j / LANES.
     const bool routed = a.dweights != nullptr;
-    int id[kSlots];
-    float l[kSlots], dw[kSlots];
+    // The loss's factors, the same for all tokens.
+    float c[PER], scale = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kSlots; ++i) {
-        const int j = lane + LANES * i;
-        id[i] = -1, l[i] = -INFINITY, dw[i] = 0.0f;
-        if (routed && j < a.k) {
-            id[i] = a.ids[t * a.k + j];
-            dw[i] = a.dweights[t * a.k + j];
-        }
-        if (id[i] < 0 || id[i] >= E) id[i] = -1;
-        else l[i] = T::load(((const typename T::type*)a.logits)[t * a.stride + id[i]]);
-        if (l[i] == -INFINITY) id[i] = -1;                  // an expert that cannot be used
-    }
-    s.make();
-    const float inv = s.sum == 0.0f ? 0.0f : 1.0f / s.sum;
-    float grad[PER];
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        s.p[i] *= inv;
-        grad[i] = 0.0f;
-    }
+    for (int i = 0; i < PER; ++i) c[i] = 0.0f;
     if (a.counts != nullptr) {
-        float c[PER], all = 0.0f, mean = 0.0f;
+        float all = 0.0f;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             c[i] = e0 + i < E ? (float)a.counts[e0 + i] : 0.0f;
             all += c[i];
-            mean += c[i] * s.p[i];
         }
         all = lanes_sum<LANES>(all);
-        mean = lanes_sum<LANES>(mean);
-        const float tokens = fmaxf((float)a.counts[E], 1.0f);
-        const float scale = *a.dloss * ((float)E / (fmaxf(all, 1.0f) * tokens));
-#pragma unroll
-        for (int i = 0; i < PER; ++i) grad[i] = scale * s.p[i] * (c[i] - mean);
+        scale = *a.dloss * ((float)E / (fmaxf(all, 1.0f) * fmaxf((float)a.counts[E], 1.0f)));
     }
-    if (routed) {
-        float peak = s.peak, sum = 0.0f, mean = 0.0f, w[kSlots];
-        if (a.renormalize) {
-            peak = l[0];
-#pragma unroll
-            for (int i = 1; i < kSlots; ++i) peak = fmaxf(peak, l[i]);
-            peak = lanes_peak<LANES>(peak);
-        }
+    Softmax<LANES, PER> s;
+    load_logits<DT>(a.logits, t * a.stride, e0, E, wide, s.p);
+    for (;;) {
+        // Lane j % LANES holds choice j in slot j / LANES.
+        int id[kSlots];
+        float l[kSlots], dw[kSlots];
 #pragma unroll
         for (int i = 0; i < kSlots; ++i) {
-            w[i] = id[i] >= 0 ? exp_down(l[i] - peak) : 0.0f;
-            sum += w[i];
+            const int j = lane + LANES * i;
+            id[i] = -1, l[i] = -INFINITY, dw[i] = 0.0f;
+            if (routed && j < a.k) {
+                id[i] = a.ids[t * a.k + j];
+                dw[i] = a.dweights[t * a.k + j];
+            }
+            if (id[i] < 0 || id[i] >= E) id[i] = -1;
+            else l[i] = T::load(((const typename T::type*)a.logits)[t * a.stride + id[i]]);
+            if (l[i] == -INFINITY) id[i] = -1;                  // an expert that cannot be used
         }
-        const float per = a.renormalize ? 1.0f / lanes_sum<LANES>(sum) : inv;
+        float next[PER];
+        if (t + step < a.T) load_logits<DT>(a.logits, (t + step) * a.stride, e0, E, wide, next);
+        s.make();
+        const float inv = s.sum == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(s.sum);
+        float grad[PER];
 #pragma unroll
-        for (int i = 0; i < kSlots; ++i) {
-            w[i] = id[i] >= 0 ? w[i] * per : 0.0f;
-            mean += id[i] >= 0 ? w[i] * dw[i] : 0.0f;
+        for (int i = 0; i < PER; ++i) {
+            s.p[i] *= inv;
+            grad[i] = 0.0f;
         }
-        mean = lanes_sum<LANES>(mean);
-        if (!a.renormalize) {
+        if (a.counts != nullptr) {
+            float mean = 0.0f;
 #pragma unroll
-            for (int i = 0; i < PER; ++i) grad[i] -= s.p[i] * mean;
+            for (int i = 0; i < PER; ++i) mean += c[i] * s.p[i];
+            mean = lanes_sum<LANES>(mean);
+#pragma unroll
+            for (int i = 0; i < PER; ++i) grad[i] = scale * s.p[i] * (c[i] - mean);
         }
-        // To the experts' lanes through LDS (the wave's own part of it).  Where a token names an
-        // expert twice, a choice does not find its own number again: then one by one.
-        float* mark = turn[group];
-        auto settle = [] {
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-            __builtin_amdgcn_wave_barrier();
-        };
-        bool twice = false;
+        if (routed) {
+            float peak = s.peak, sum = 0.0f, mean = 0.0f, w[kSlots];
+            if (a.renormalize) {
+                peak = l[0];
 #pragma unroll
-        for (int i = 0; i < kSlots; ++i)
-            if (id[i] >= 0) mark[id[i]] = (float)(lane + LANES * i);
-        settle();
+                for (int i = 1; i < kSlots; ++i) peak = fmaxf(peak, l[i]);
+                peak = lanes_peak<LANES>(peak);
+            }
 #pragma unroll
-        for (int i = 0; i < kSlots; ++i)
-            if (id[i] >= 0) twice = twice || mark[id[i]] != (float)(lane + LANES * i);
-        settle();
-        float add[PER];
+            for (int i = 0; i < kSlots; ++i) {
+                w[i] = id[i] >= 0 ? exp_down(l[i] - peak) : 0.0f;
+                sum += w[i];
+            }
+            const float per = a.renormalize ? __builtin_amdgcn_rcpf(lanes_sum<LANES>(sum)) : inv;
 #pragma unroll
-        for (int i = 0; i < PER; ++i) turn[group][e0 + i] = 0.0f;
-        settle();
-        const bool one_by_one = __any(twice);
+            for (int i = 0; i < kSlots; ++i) {
+                w[i] = id[i] >= 0 ? w[i] * per : 0.0f;
+                mean += id[i] >= 0 ? w[i] * dw[i] : 0.0f;
+            }
+            mean = lanes_sum<LANES>(mean);
+            if (!a.renormalize) {
 #pragma unroll
-        for (int i = 0; i < kSlots; ++i) {
-            const float mine = a.renormalize ? w[i] * (dw[i] - mean) : w[i] * dw[i];
-            if (!one_by_one) {
-                if (id[i] >= 0) turn[group][id[i]] = mine;
-            } else {
-                for (int j = 0; j < LANES; ++j) {
-                    if (lane == j && id[i] >= 0) turn[group][id[i]] += mine;
-                    settle();
+                for (int i = 0; i < PER; ++i) grad[i] -= s.p[i] * mean;
+            }
+            // To the experts' lanes through LDS (the wave's own part of it).  Where a token names an
+            // expert twice, a choice does not find its own number again: then one by one.
+            float* mark = turn[group];
+            auto settle = [] {
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                __builtin_amdgcn_wave_barrier();
+            };
+            bool twice = false;
+#pragma unroll
+            for (int i = 0; i < kSlots; ++i)
+                if (id[i] >= 0) mark[id[i]] = (float)(lane + LANES * i);
+            settle();
+#pragma unroll
+            for (int i = 0; i < kSlots; ++i)
+                if (id[i] >= 0) twice = twice || mark[id[i]] != (float)(lane + LANES * i);
+            settle();
+            float add[PER];
+#pragma unroll
+            for (int i = 0; i < PER; ++i) turn[group][e0 + i] = 0.0f;
+            settle();
+            const bool one_by_one = __any(twice);
+#pragma unroll
+            for (int i = 0; i < kSlots; ++i) {
+                const float mine = a.renormalize ? w[i] * (dw[i] - mean) : w[i] * dw[i];
+                if (!one_by_one) {
+                    if (id[i] >= 0) turn[group][id[i]] = mine;
+                } else {
+                    for (int j = 0; j < LANES; ++j) {
+                        if (lane == j && id[i] >= 0) turn[group][id[i]] += mine;
+                        settle();
+                    }
                 }
             }
+            settle();
+#pragma unroll
+            for (int i = 0; i < PER; ++i) add[i] = turn[group][e0 + i];
+#pragma unroll
+            for (int i = 0; i < PER; ++i) grad[i] += add[i];
         }
-        settle();
+        typename T::type* out = (typename T::type*)a.dlogits + t * E + e0;
+        typename T::type o[PER];
 #pragma unroll
-        for (int i = 0; i < PER; ++i) add[i] = turn[group][e0 + i];
+        for (int i = 0; i < PER; ++i) o[i] = T::store(grad[i]);
+        if (wide_out && e0 + PER <= E) {
+            __builtin_memcpy(__builtin_assume_aligned(out, 16), o, sizeof(o));
+        } else {
 #pragma unroll
-        for (int i = 0; i < PER; ++i) grad[i] += add[i];
-    }
-    typename T::type* out = (typename T::type*)a.dlogits + t * E + e0;
-    typename T::type o[PER];
+            for (int i = 0; i < PER; ++i)
+                if (e0 + i < E) out[i] = o[i];
+        }
+        t += step;
+        if (t >= a.T) return;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) o[i] = T::store(grad[i]);
-    if (wide_out && e0 + PER <= E) {
-        __builtin_memcpy(__builtin_assume_aligned(out, 16), o, sizeof(o));
-    } else {
-#pragma unroll
-        for (int i = 0; i < PER; ++i)
-            if (e0 + i < E) out[i] = o[i];
+    for (int i = 0; i < PER; ++i) s.p[i] = next[i];
     }
 }
 
@@ -529,8 +546,9 @@ hipError_t launch_route_grad(const RouteGradArgs& a, DType dt, hipStream_t strea
         by_experts(a.E, [&](auto n) {
             typedef decltype(n) L;
             constexpr int kTokens = 256 / L::lanes;
+            const int blocks = (a.T + kTokens - 1) / kTokens, most = 4 * 256;   // several tokens a lane
             route_grad_kernel<decltype(d)::value, L::lanes, L::per>
-                <<<(unsigned)((a.T + kTokens - 1) / kTokens), 256, 0, stream>>>(a, wide, wide_out);
+                <<<blocks < most ? blocks : most, 256, 0, stream>>>(a, wide, wide_out);
         });
     });
     return hipGetLastError();
