@@ -134,6 +134,26 @@ def test_route_grad_any_ids_and_strides(mx, dtype, renormalize):  # noqa: F811
     assert (got[10:13] == 0).all()
 
 
+@pytest.mark.parametrize("dtype", FLOATS)
+@pytest.mark.parametrize("E", [7, 100, 300, 600])
+@pytest.mark.parametrize("renormalize", [True, False])
+def test_masks_of_the_lowest_value(mx, dtype, E, renormalize):  # noqa: F811
+    """The type's lowest value as a mask: an expert like another (a row of it is uniform), as small
+    as it is; beside -infinity; and logits far apart."""
+    rng = np.random.default_rng(E)
+    low = torch.finfo(dtype).min
+    x = gpu(rng.standard_normal((12, E)), dtype)
+    x[0], x[1, 1:], x[2, ::2] = low, low, low
+    x[3], x[3, 4] = float("-inf"), low
+    x[4, :3], x[5, 3:] = low, torch.finfo(dtype).max / 4
+    x[6], x[6, 1] = 0.0, -150.0
+    ids, _ = mx.route(x, 3)
+    counts = check_balance(mx, x, ids)
+    assert int(counts[E]) == 12
+    check_route_grad(mx, x, ids, gpu(rng.standard_normal((12, 3)), torch.float32), renormalize, counts,
+                     torch.full((), 30.0, device="cuda"))
+
+
 def test_route_grad_not_finite_rows_stay_rows(mx):  # noqa: F811
     rng = np.random.default_rng(1)
     x = gpu(rng.standard_normal((12, 20)), torch.float32)
