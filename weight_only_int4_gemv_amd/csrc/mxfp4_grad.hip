@@ -248,6 +248,12 @@ __global__ __launch_bounds__(kWaves* kWave) void stream_grad_kernel(GradArgs a) 
 // In LDS, 16-byte chunk c of row m of dY stands at c ^ x_swizzle(m): 16 lanes that read one chunk
 // of 16 rows meet all banks once.  Of each 32 weight rows, row 8 g + i has place 4 i + g (lane
 // groups g = 0 .. 3 read one i together) and chunk c of it stands at c ^ w_swizzle(g).
+//
+// 3001 rows, 14336 x 4096, fp16: 353 us, 1.0 PFLOP/s (512 tiles of 96 rows, two a CU, fill one round);
+// 8192 tokens' rows of 64 experts of 3584 x 4096: 875 us, 1.1 PFLOP/s.  Blocks of 2 x 2 waves, which
+// convert each weight twice, took 475 us for the first, 256 x 256 with a wave a SIMD 619 (bf16).  32 rows
+// each of 64 experts: 197 us, and 231 without s_setprio around the products, 225 to 244 with the scales'
+// conversion put off by a step or the copies spread between the products.
 constexpr int kStep = 64;
 constexpr int kXRow = kStep * 2;                            // bytes of a row of the dY tile
 constexpr int kTiledWaves = 4, kTiledThreads = kTiledWaves * kWave;
@@ -358,23 +364,38 @@ __global__ __launch_bounds__(kTiledThreads, C::kPerCu) void tiled_grad_kernel(Gr
     const bool words = KB % 4 == 0 && (uintptr_t)a.scales % 4 == 0;
     const int kb0 = k0 / kBlock, s_row0 = (wave & 1) * kStepRows;
     const uint32_t s_off = (uint32_t)(s_row0 + lane / 2) * KB + (kb0 + (lane & 1) * 4 < KB ? (lane & 1) * 4 : 0);
-    auto copy_scales = [&](int s) {
+    const uint8_t* s_base = a.scales + (expert_row + (int64_t)step0 * kStep) * KB + kb0;
+    uint32_t s_to = 0;
+    auto copy_scales = [&](int s) {                         // one step after the other
         if (!words || s >= steps) return;
         const int n0 = (step0 + s) * kStep;
         uint32_t off = s_off;                               // rows past N: the last row's
         if (n0 + kStep > a.N) off -= (uint32_t)max(n0 + s_row0 + lane / 2 - (a.N - 1), 0) * KB;
-        copy4(a.scales + (expert_row + n0) * KB + kb0, off,
-              __builtin_amdgcn_readfirstlane(base + C::kBytes + s % kStages * kScales + s_row0 * kBlocks));
+        copy4(s_base, off, __builtin_amdgcn_readfirstlane(base + C::kBytes + s_to + s_row0 * kBlocks));
+        s_base += kStep * KB;
+        s_to = s_to + kScales == kStages * kScales ? 0 : s_to + kScales;
     };
     uint32_t to = 0;                                        // LDS offset of the copied stage
     auto copy = [&](int s) {
         const int n0 = (step0 + s) * kStep;
         const uint32_t x_to = base + to + wave * 8 * kXRow;
         const uint32_t w_to = base + to + C::kXBytes + wave * 2 * 8 * kWRow;
-        if (WIDE && t.rows == C::BM && n0 + kStep <= a.N) {
+        if (WIDE && n0 + kStep <= a.N) {
+            if (t.rows == C::BM) {
 #pragma unroll
-            for (int c = 0; c < C::kXCopies; ++c)
-                copy16(x_base + c * x_next, x_off, x_to + c * kXRows * kXRow);
+                for (int c = 0; c < C::kXCopies; ++c)
+                    copy16(x_base + c * x_next, x_off, x_to + c * kXRows * kXRow);
+            } else {
+                // Rows past the tile: its last row, for dX rows that are not stored.
+                int l = lane;                               // for no register to stay taken
+                asm volatile("" : "+v"(l));
+#pragma unroll
+                for (int c = 0; c < C::kXCopies; ++c) {
+                    const int row = min(wave * 8 + l / 8, t.rows - 1 - c * kXRows);
+                    const uint32_t off = (uint32_t)(max(row, 0) * (uint32_t)a.y_stride + x_chunk * 8) * 2;
+                    copy16(x_base + (c * kXRows < t.rows ? c * x_next : 0), off, x_to + c * kXRows * kXRow);
+                }
+            }
 #pragma unroll
             for (int j = 0; j < kWCopies; ++j)
                 copy16(w_base + 2 * j * row_bytes, w_off, w_to + j * 8 * kWRow);
@@ -685,8 +706,8 @@ struct Choice {
     Kernel kernel;
     int slices, steps;
 };
-// A step of 64 weight rows takes kOne us with a block on a CU and kTwo with two of them (M x 4096,
-// 8192 weight rows); a launch begins and ends with the time of about three.
+// A step of 64 weight rows takes `one` us with a block on a CU and `two` with two of them (measured on
+// M x 4096, 8192 weight rows); a launch begins and ends with the time of about three steps.
 struct Cost {
     Kernel kernel;
     int rows;
