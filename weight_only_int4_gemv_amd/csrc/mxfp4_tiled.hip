@@ -462,6 +462,7 @@ __global__ __launch_bounds__(C::kThreads, C::kPerCu * C::kWaves / 4) void tiled_
 }
 
 typedef Tiling<128, 64, 4, 3, 16, 2> Large;         // 128 x 256
+typedef Tiling<96, 64, 4, 3, 16, 2> Mid;            // 96 x 256
 typedef Tiling<64, 64, 4, 3, 8, 3> Medium;          // 64 x 256
 typedef Tiling<32, 64, 4, 4, 8, 3> Low;             // 32 x 256
 typedef Tiling<64, 32, 4, 4, 16, 3> Narrow;         // 64 x 128
@@ -502,7 +503,7 @@ void launch(LinearArgs a, DType dt, hipStream_t stream) {
 //   K slices (dense): where the tiles are fewer than the blocks that fit on 256
 //   CUs, as many as fill two a CU, of at least eight steps: 50 x 4096 x 14336
 //   105 us unsplit, 24 in 8 or 16 slices; 17 rows 30 and 20 us.
-enum Kernel { kStream, kLow, kNarrow, kMedium, kLarge };
+enum Kernel { kStream, kLow, kNarrow, kMedium, kMid, kLarge };
 struct Choice {
     Kernel kernel;
     int slices, steps;
@@ -535,22 +536,29 @@ Choice choose(int64_t R, int64_t E, int64_t N, int64_t K, bool grouped, bool spl
 
 // Kernel and K split of a dense product with an epilogue: as above up to 32 rows, else the least of
 // what tilings and slices take.  With 4096 columns a block of Large takes 53 us beside another (64
-// alone), of Medium 31.5 and of Narrow 18.9, and they add up over the blocks of a CU (14336 weight
-// rows, 701 rows: 103 / 98 / 105 us, 300 rows 64 / 62 / 55, 2000 rows 227 / 246 / 283; 4096 x 14336,
-// 701 rows: 129 us unsplit, 102 in 4 slices of Medium).  A second launch adds the slices' sums.
+// alone), a pair of Mid 93 (53 alone), of Medium 31.5 and of Narrow 18.9, and they add up over the
+// blocks of a CU (14336 weight rows, 701 rows: Large 103, Mid 98, Medium 105, Narrow 105 us, 300 rows
+// 64 / 61 / 62 / 55, 2000 rows 227 / 249 / 246 / 283; 4096 x 4096, 3001 rows: 124 and of Mid 107;
+// 4096 x 14336, 701 rows: 129 us unsplit, 102 in 4 slices of Medium).  A second launch adds the
+// slices' sums.
 Choice choose_act(int64_t R, int64_t N, int64_t K, bool split) {
     Choice best = choose(R, 1, N, K, false, split);
     if (R <= 32) return best;
     const int64_t total = (K / kBlock + 1) / 2;
     double least = 0;
-    for (const Kernel kernel : {kLarge, kMedium, kNarrow}) {
-        const int bm = kernel == kLarge ? 128 : 64, bn = kernel == kNarrow ? 128 : 256;
+    for (const Kernel kernel : {kLarge, kMid, kMedium, kNarrow}) {
+        const int bm = kernel == kLarge ? 128 : kernel == kMid ? 96 : 64, bn = kernel == kNarrow ? 128 : 256;
         const int64_t tiles = (R + bm - 1) / bm * ((N + bn - 1) / bn);
         for (int64_t s = 1; s <= (split ? 8 : 1) && (s == 1 || total / s >= 8); ++s) {
             const int64_t steps = total > 0 ? (total + s - 1) / s : 1, slices = total > 0 ? (total + steps - 1) / steps : 1;
             const double n = double(tiles * slices) / 256, cus = n > 1 ? (double)(int64_t)(n + 0.999) : 1;
-            double us = kernel == kLarge ? 10 + 53 * cus : kernel == kMedium ? 25 + 31.5 * n : 12 + 18.9 * n;
+            const int64_t pairs = tiles * slices / 512, left = tiles * slices % 512;
+            double us = kernel == kLarge    ? 10 + 53 * cus
+                        : kernel == kMid    ? 93.0 * pairs + (left > 256 ? 93 : left > 0 ? 53 : 0)
+                        : kernel == kMedium ? 25 + 31.5 * n
+                                            : 12 + 18.9 * n;
             us *= double(steps) / 64;
+            if (kernel == kMid) us += 4;                    // of a launch, however short its blocks
             if (slices > 1) us += 5 + double(slices) * R * N * 8 / 8e6;
             if (least == 0 || us < least) {
                 least = us;
@@ -584,7 +592,7 @@ hipError_t launch_linear(LinearArgs a, DType dt, float* part, hipStream_t stream
         case kLow: launch<Low>(a, dt, stream); break;
         case kNarrow: launch<Narrow>(a, dt, stream); break;
         case kMedium: launch<Medium>(a, dt, stream); break;
-        case kLarge: launch<Large>(a, dt, stream); break;
+        default: launch<Large>(a, dt, stream); break;
     }
     if (c.slices > 1) launch_add_slices(a.part, a.slices, (int64_t)a.R * a.N, a.Y, dt, stream);
     return hipGetLastError();
@@ -610,6 +618,7 @@ hipError_t launch_linear_act(LinearArgs a, DType dt, float* part, hipStream_t st
         case kLow: launch<Low>(a, dt, stream); break;
         case kNarrow: launch<Narrow>(a, dt, stream); break;
         case kMedium: launch<Medium>(a, dt, stream); break;
+        case kMid: launch<Mid>(a, dt, stream); break;
         case kLarge: launch<Large>(a, dt, stream); break;
     }
     const hipError_t e = hipGetLastError();
