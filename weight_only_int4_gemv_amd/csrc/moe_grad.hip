@@ -115,7 +115,9 @@ inline bool wide_rows(const void* p, int64_t stride, DType dt) {
 // loss = E sum_e (c_e / C) (S_e / T'): c_e the choices of expert e, C their sum, S_e the sum of
 // the tokens' softmax at e, T' the tokens that may use an expert.  Lanes add their tokens' shares;
 // blocks leave sums [block][E] and counts [block][E + 1] to a second launch, which adds them in
-// order: the result does not depend on scheduling.
+// order: the result does not depend on scheduling.  65521 tokens of 128 bf16 logits (16.8 MB and
+// 2 MB of choices): 12 us of instruction issue and 6 us for the second launch, one block's latency;
+// adding the blocks with atomics would save the launch and the fixed order.
 constexpr int kBalanceThreads = 512;
 constexpr int kMaxBalanceBlocks = 256;
 
@@ -391,7 +393,7 @@ __global__ __launch_bounds__(256) void route_grad_kernel(RouteGradArgs a, bool w
         t += step;
         if (t >= a.T) return;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) s.p[i] = next[i];
+        for (int i = 0; i < PER; ++i) s.p[i] = next[i];
     }
 }
 
@@ -401,7 +403,9 @@ __global__ __launch_bounds__(256) void route_grad_kernel(RouteGradArgs a, bool w
 // positions[t, j].  A wave per choice: it reads both rows once (the token's other choices find
 // dout in the caches) and writes dY's row if tokens[r] names the token and no earlier choice of
 // it the row; a row that no choice of its token names gets zeros from wave r.  So every row of
-// dY is written once whatever the tensors hold.
+// dY is written once whatever the tensors hold.  Bound by HBM: 6000 tokens, one in
+// sixteen of them padding, the others with eight rows of 4096 (787 MB), take 151 us, 5.2 TB/s; with one
+// piece of the rows in hand 173.
 template <typename T, typename ROW, int VEC>
 __global__ __launch_bounds__(256) void combine_grad_kernel(const uint16_t* dout, const void* Y_,
                                                            int R, int N, const int* tokens,

@@ -249,11 +249,12 @@ __global__ __launch_bounds__(kWaves* kWave) void stream_grad_kernel(GradArgs a) 
 // of 16 rows meet all banks once.  Of each 32 weight rows, row 8 g + i has place 4 i + g (lane
 // groups g = 0 .. 3 read one i together) and chunk c of it stands at c ^ w_swizzle(g).
 //
-// 3001 rows, 14336 x 4096, fp16: 353 us, 1.0 PFLOP/s (512 tiles of 96 rows, two a CU, fill one round);
-// 8192 tokens' rows of 64 experts of 3584 x 4096: 875 us, 1.1 PFLOP/s.  Blocks of 2 x 2 waves, which
-// convert each weight twice, took 475 us for the first, 256 x 256 with a wave a SIMD 619 (bf16).  32 rows
-// each of 64 experts: 197 us, and 231 without s_setprio around the products, 225 to 244 with the scales'
-// conversion put off by a step or the copies spread between the products.
+// 3001 rows, 14336 x 4096, fp16: 352 us in a long row of calls, 302 to 331 in a short one, 1.0 to 1.15
+// PFLOP/s (512 tiles of 96 rows, two a CU, fill one round); 8192 tokens' rows of 64 experts of 3584 x
+// 4096: 856 us, 1.05 PFLOP/s.  Blocks of 2 x 2 waves, which convert each weight twice, took 475 us for
+// the first, 256 x 256 with a wave a SIMD 619 (bf16).  32 rows each of 64 experts: 197 us, and 231
+// without s_setprio around the products, 225 to 244 with the scales' conversion put off by a step or
+// the copies spread between the products.
 constexpr int kStep = 64;
 constexpr int kXRow = kStep * 2;                            // bytes of a row of the dY tile
 constexpr int kTiledWaves = 4, kTiledThreads = kTiledWaves * kWave;
