@@ -223,6 +223,36 @@ def test_grouped_linear_grad(mx, dtype, name, N, K):  # noqa: F811
             ref.check(got, want, bound + ref.rounded(np.abs(want), out), out)
 
 
+@pytest.mark.parametrize("dtype", HALVES)
+@pytest.mark.parametrize("rows", [(3, 0, 17, 1), (17, 0, 33, 1), (40, 31, 50, 1), (97, 65, 1, 100),
+                                  (129, 40, 250, 3)])
+@pytest.mark.parametrize("N,pad", [(320, 8), (333, 3)])
+def test_part_filled_tiles(mx, dtype, rows, N, pad):  # noqa: F811
+    """Tiles of every height with fewer rows than they hold, rows of dY apart with NaN between: an
+    expert's last row, which may stand for those that are not there, changes no other row, nor does a
+    neighbour's."""
+    K, R = 544, sum(rows)
+    say("part-filled tiles %s %s N=%d" % (dtype, rows, N))
+    rng = np.random.default_rng([N, R])
+    codes, scales = weights(rng, (4, N, K))
+    offsets = np.concatenate([[0], np.cumsum(rows)])
+    room = torch.full((R, N + pad), float("nan"), dtype=dtype, device="cuda")
+    dy = room[:, :N]
+    dy.copy_(gpu(rng.standard_normal((R, N)), dtype))
+    args = gpu(codes), gpu(scales), gpu(offsets.astype(np.int32))
+    got = mx.grouped_linear_grad(dy, *args)
+    for e in range(4):
+        lo, hi = offsets[e], offsets[e + 1]
+        ref.check(got[lo:hi], *expect(ref.f64(dy[lo:hi]), codes[e], scales[e], dtype), dtype)
+    last = torch.tensor([int(offsets[e + 1]) - 1 for e in range(4) if rows[e]], device="cuda")
+    dy[last] = float("nan")
+    spoilt = mx.grouped_linear_grad(dy, *args)
+    assert spoilt[last].isnan().all()
+    keep = torch.ones(R, dtype=torch.bool, device="cuda")
+    keep[last] = False
+    assert torch.equal(spoilt[keep], got[keep])
+
+
 def test_grouped_experts_past_32_bits(mx):  # noqa: F811
     """Codes of more than 2^32 bytes: the last experts' weights lie past 32-bit offsets."""
     E, N, K = 5, 65536, 32768
