@@ -78,6 +78,16 @@ def test_linear_act(mx, dtype, act, M, N, K):
 
 
 @pytest.mark.parametrize("dtype", HALVES)
+@pytest.mark.parametrize("act,M,N,K,low", [("gelu_tanh", 150, 28501, 2048, 118), ("swiglu", 150, 28500, 2048, 100),
+                                           ("relu", 187, 6200, 8192, 118)])
+def test_linear_act_tiles_of_96_rows(mx, dtype, act, M, N, K, low):
+    """Whole tiles and part-filled ones, with scales on both sides of fp16's range, and in K slices."""
+    say("linear_act 96 rows %s %s M=%d N=%d K=%d" % (dtype, act, M, N, K))
+    check_linear(mx, np.random.default_rng([M, N, K]), M, N, K, dtype, act, residual=act == "relu",
+                 low=low)
+
+
+@pytest.mark.parametrize("dtype", HALVES)
 @pytest.mark.parametrize("act", ["none", "gelu", "swiglu"])
 @pytest.mark.parametrize("N,K", [(4096, 4096), (1198, 14336), (16390, 1056), (66000, 256), (3500, 14976)])
 def test_linear_act_one_row_of_many_weights(mx, dtype, act, N, K):
