@@ -192,7 +192,7 @@ enum {
  *   Y        out: [M, F] of X's dtype, dense
  *   Z        out: [M, N] of X's dtype, dense: z, for the backward pass; or NULL
  * Sums, z and the activation are fp32; Y and Z are rounded once each.
- * workspace as for mxfp4_linear, with its own size. */
+ * workspace as for mxfp4_linear, with its own size, which is that of any activation. */
 size_t mxfp4_linear_act_workspace_bytes(int64_t M, int64_t N, int64_t K);
 int mxfp4_linear_act(const void* X, int dtype, int64_t M, int64_t x_stride, const uint8_t* codes,
                      const uint8_t* scales, int64_t N, int64_t K, const void* bias,

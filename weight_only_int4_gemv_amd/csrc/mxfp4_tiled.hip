@@ -541,31 +541,44 @@ Choice choose(int64_t R, int64_t E, int64_t N, int64_t K, bool grouped, bool spl
 // 64 / 61 / 62 / 55, 2000 rows 227 / 249 / 246 / 283; 4096 x 4096, 3001 rows: 124 and of Mid 107;
 // 4096 x 14336, 701 rows: 129 us unsplit, 102 in 4 slices of Medium).  A second launch adds the
 // slices' sums.
-Choice choose_act(int64_t R, int64_t N, int64_t K, bool split) {
+//
+// Unsplit SwiGLU does not run on Narrow: a wave's 32 weight rows have no place for a gate and its up
+// rows.  Where Narrow unsplit is the least, SwiGLU takes the least of the rest without Large, whose
+// time of a short call is longer than said above (180 x 28672 x 1024: Large 26.4 us, Medium 24.1; 100
+// x 14336 x 2048: Large in 4 slices 26.6, Narrow in 2 23.7).  Against Medium unsplit: 100 x 2048 x 2048
+// 25.9 and in 4 slices of Narrow 13.4 us, 64 x 28672 x 4096 49.6 and in 2 34.9, 300 x 4096 x 4096 45.4
+// and in 4 29.4, 300 x 14336 x 4096 64.2 and of Mid 57.1; 128 x 4096 x 256 9.4, where it stays.
+Choice choose_act(int64_t R, int64_t N, int64_t K, bool split, bool swiglu) {
     Choice best = choose(R, 1, N, K, false, split);
     if (R <= 32) return best;
     const int64_t total = (K / kBlock + 1) / 2;
-    double least = 0;
-    for (const Kernel kernel : {kLarge, kMid, kMedium, kNarrow}) {
-        const int bm = kernel == kLarge ? 128 : kernel == kMid ? 96 : 64, bn = kernel == kNarrow ? 128 : 256;
-        const int64_t tiles = (R + bm - 1) / bm * ((N + bn - 1) / bn);
-        for (int64_t s = 1; s <= (split ? 8 : 1) && (s == 1 || total / s >= 8); ++s) {
-            const int64_t steps = total > 0 ? (total + s - 1) / s : 1, slices = total > 0 ? (total + steps - 1) / steps : 1;
-            const double n = double(tiles * slices) / 256, cus = n > 1 ? (double)(int64_t)(n + 0.999) : 1;
-            const int64_t pairs = tiles * slices / 512, left = tiles * slices % 512;
-            double us = kernel == kLarge    ? 10 + 53 * cus
-                        : kernel == kMid    ? 93.0 * pairs + (left > 256 ? 93 : left > 0 ? 53 : 0)
-                        : kernel == kMedium ? 25 + 31.5 * n
-                                            : 12 + 18.9 * n;
-            us *= double(steps) / 64;
-            if (kernel == kMid) us += 4;                    // of a launch, however short its blocks
-            if (slices > 1) us += 5 + double(slices) * R * N * 8 / 8e6;
-            if (least == 0 || us < least) {
-                least = us;
-                best = Choice{kernel, (int)slices, (int)steps};
+    auto least_of = [&](bool all) {
+        double least = 0;
+        for (const Kernel kernel : {kLarge, kMid, kMedium, kNarrow}) {
+            if (!all && kernel == kLarge) continue;
+            const int bm = kernel == kLarge ? 128 : kernel == kMid ? 96 : 64, bn = kernel == kNarrow ? 128 : 256;
+            const int64_t tiles = (R + bm - 1) / bm * ((N + bn - 1) / bn);
+            for (int64_t s = 1; s <= (split ? 8 : 1) && (s == 1 || total / s >= 8); ++s) {
+                const int64_t steps = total > 0 ? (total + s - 1) / s : 1, slices = total > 0 ? (total + steps - 1) / steps : 1;
+                if (!all && kernel == kNarrow && slices == 1) continue;
+                const double n = double(tiles * slices) / 256, cus = n > 1 ? (double)(int64_t)(n + 0.999) : 1;
+                const int64_t pairs = tiles * slices / 512, left = tiles * slices % 512;
+                double us = kernel == kLarge    ? 10 + 53 * cus
+                            : kernel == kMid    ? 93.0 * pairs + (left > 256 ? 93 : left > 0 ? 53 : 0)
+                            : kernel == kMedium ? 25 + 31.5 * n
+                                                : 12 + 18.9 * n;
+                us *= double(steps) / 64;
+                if (kernel == kMid) us += 4;                // of a launch, however short its blocks
+                if (slices > 1) us += 5 + double(slices) * R * N * 8 / 8e6;
+                if (least == 0 || us < least) {
+                    least = us;
+                    best = Choice{kernel, (int)slices, (int)steps};
+                }
             }
         }
-    }
+    };
+    least_of(true);
+    if (swiglu && best.kernel == kNarrow && best.slices == 1) least_of(false);
     return best;
 }
 
@@ -579,7 +592,8 @@ size_t linear_workspace(int64_t M, int64_t N, int64_t K) {
 
 size_t linear_act_workspace(int64_t M, int64_t N, int64_t K) {
     if (M <= 0 || N <= 0) return 0;
-    const Choice c = choose_act(M, N, K, true);
+    // Of any activation: SwiGLU may take slices where the others do not.
+    const Choice c = choose_act(M, N, K, true, true);
     return c.slices > 1 ? (size_t)c.slices * M * N * sizeof(float) : 0;
 }
 
@@ -602,16 +616,14 @@ hipError_t launch_linear(LinearArgs a, DType dt, float* part, hipStream_t stream
 // second launch, which has to read them anyway.
 hipError_t launch_linear_act(LinearArgs a, DType dt, float* part, hipStream_t stream) {
     if (a.offsets == nullptr && gemv_fits(a.R, a.N, a.K)) return launch_gemv(a, dt, stream);
-    Choice c = a.offsets != nullptr ? choose(a.R, a.E, a.N, a.K, true, false)
-                                    : choose_act(a.R, a.N, a.K, part != nullptr);
+    const Choice c = a.offsets != nullptr ? choose(a.R, a.E, a.N, a.K, true, false)
+                                          : choose_act(a.R, a.N, a.K, part != nullptr, a.act == kSwiglu);
     a.slices = c.slices, a.steps = c.steps;
     if (c.slices > 1) {
         a.part = part;
     } else {
         a.epilogue = true;
         a.swiglu = a.act == kSwiglu;
-        // A wave of Narrow has no place for a gate and its up rows.
-        if (a.swiglu && c.kernel == kNarrow) c.kernel = kMedium;
     }
     switch (c.kernel) {
         case kStream: return launch_stream(a, dt, stream);
