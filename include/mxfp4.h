@@ -262,7 +262,8 @@ int mxfp4_grouped_linear_grad(const void* dY, int dtype, int64_t R, int64_t y_st
  *   workspace DEVICE, 4-byte aligned, at least moe_balance_workspace_bytes(T, E, k)
  *             bytes (may be NULL where that is 0); no initial contents needed, in use
  *             until the call's work on the stream has finished.
- * A logit of NaN or +infinity makes the loss NaN.  T k <= 2^29. */
+ * A logit of NaN or +infinity makes the loss NaN (and its token counts in T').
+ * T k <= 2^29. */
 size_t moe_balance_workspace_bytes(int64_t T, int64_t E, int64_t k);
 int moe_balance(const void* logits, int dtype, int64_t T, int64_t E, int64_t stride,
                 const int32_t* ids, int64_t k, float* loss, int32_t* counts, void* workspace,
@@ -279,8 +280,11 @@ int moe_balance(const void* logits, int dtype, int64_t T, int64_t E, int64_t str
  *                 where a loss spans several batches), or NULL (no such part)
  *   dloss    in : fp32, one value, with counts
  *   dlogits  out: [T, E] of the logits' dtype, dense.  0 for an expert at
- *                 -infinity.
- * A row with a NaN or +infinity has NaN gradients. */
+ *                 -infinity, where the row has no NaN and no +infinity.
+ * With renormalize and without counts a row's gradients depend on the logits of its
+ * chosen experts alone: a NaN or +infinity among these makes the chosen experts'
+ * gradients NaN, one elsewhere changes nothing.  In every other case a NaN or
+ * +infinity makes all of the row's gradients NaN. */
 int moe_route_grad(const void* logits, int dtype, int64_t T, int64_t E, int64_t stride,
                    const int32_t* ids, int64_t k, const float* dweights, int renormalize,
                    const int32_t* counts, const float* dloss, void* dlogits, void* stream);

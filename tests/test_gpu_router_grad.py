@@ -1,0 +1,74 @@
+"""The balance loss and the router's gradient on the GPU with logits that are not finite (forms and
+bounds in mxfp4_router_reference)."""
+import numpy as np
+import pytest
+
+import mxfp4_reference as ref
+import mxfp4_router_reference as rref
+from test_gpu_linear_act import gpu, mx, say  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+FLOATS = [torch.float16, torch.bfloat16, torch.float32]
+
+
+def check_balance(mx, x, ids):  # noqa: F811
+    loss, counts = mx.balance(x, ids)
+    want, bound, n = rref.balance(ref.f64(x), ids.cpu().numpy())
+    assert np.array_equal(counts.cpu().numpy(), n)
+    assert abs(float(loss) - want) <= bound + 2.0 ** -24 * abs(want), (float(loss), want, bound)
+    return counts
+
+
+def check_route_grad(mx, x, ids, dw, renormalize, counts, dloss):  # noqa: F811
+    got = mx.route_grad(x, ids, dw, renormalize=renormalize, counts=counts, dloss=dloss)
+    want, bound = rref.route_grad(ref.f64(x), ids.cpu().numpy(), None if dw is None else ref.f64(dw),
+                                  renormalize, None if counts is None else counts.cpu().numpy(),
+                                  0.0 if dloss is None else float(dloss))
+    with np.errstate(all="ignore"):
+        ref.check(got, want, bound + ref.rounded(np.abs(want) + bound, x.dtype), x.dtype)
+    return got
+
+
+@pytest.mark.parametrize("dtype", FLOATS)
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("E", [20, 100, 300])
+def test_logits_that_are_not_finite(mx, dtype, bad, E):  # noqa: F811
+    """With renormalized weights alone the chosen logits are all that counts: one that is not finite
+    makes the chosen experts' gradients NaN, one that is not chosen changes nothing.  Without
+    renormalize, and with the loss, every gradient of the row is NaN."""
+    rng = np.random.default_rng(E)
+    x = gpu(rng.standard_normal((12, E)), torch.float32).to(dtype)
+    x[:, 7] = float("-inf")
+    ids, _ = mx.route(x, 3)
+    dw = gpu(rng.standard_normal((12, 3)), torch.float32)
+    counts, one = mx.balance(x, ids)[1], torch.ones((), device="cuda")
+    clean = {r: mx.route_grad(x, ids, dw, renormalize=r) for r in (True, False)}
+    loss = mx.route_grad(x, ids, counts=counts, dloss=one)
+    y = x.clone()
+    chosen = ids[2].tolist()
+    free = next(e for e in range(E) if e not in ids[5].tolist() and e != 7)
+    y[2, chosen[1]], y[5, free] = bad, bad
+    got = mx.route_grad(y, ids, dw)
+    assert got[2, chosen].isnan().all() and int(got[2].isnan().sum()) == 3 and (got[2].nan_to_num(0) == 0).all()
+    keep = [r for r in range(12) if r != 2]
+    assert torch.equal(got[keep], clean[True][keep])
+    rest = [r for r in range(12) if r not in (2, 5)]
+    for other, want in ((mx.route_grad(y, ids, dw, renormalize=False), clean[False]),
+                        (mx.route_grad(y, ids, counts=counts, dloss=one), loss)):
+        assert other[2].isnan().all() and other[5].isnan().all()
+        assert torch.equal(other[rest], want[rest])
+    check_route_grad(mx, y, ids, dw, True, None, None)
+    n = check_counts(mx, y, ids)
+    assert n == 12
+
+
+def check_counts(mx, y, ids):  # noqa: F811
+    loss, counts = mx.balance(y, ids)
+    assert loss.isnan()
+    only = torch.full((1, y.shape[1]), float("-inf"), dtype=y.dtype, device="cuda")
+    only[0, 1] = float("nan")                               # a NaN counts as a usable expert
+    loss, one = mx.balance(only, torch.full((1, 1), 1, dtype=torch.int32, device="cuda"))
+    assert loss.isnan() and int(one[-1]) == 1
+    return int(counts[-1])

@@ -705,7 +705,9 @@ def route_grad(logits: torch.Tensor, ids: torch.Tensor = None, dweights: torch.T
     """dlogits [T, E] of the logits' dtype: the gradient of route()'s weights for ids
     int32 [T, k] and dweights fp32 [T, k] (None: no such part), plus dloss (fp32, one
     value) times the gradient of balance()'s loss for its counts (None: no such part).
-    The choices and the counts are constants."""
+    The choices and the counts are constants.  A NaN or +inf makes all gradients of its
+    row NaN; with renormalize and without counts only the chosen experts' logits matter,
+    and only their gradients become NaN."""
     lib = library()
     T, E, k, stride = _router(logits, ids)
     if dweights is None and counts is None:
