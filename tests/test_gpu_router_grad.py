@@ -1,5 +1,6 @@
-"""The balance loss and the router's gradient on the GPU with logits that are not finite (forms and
-bounds in mxfp4_router_reference)."""
+"""The balance loss and the router's gradient on the GPU with masks of the type's lowest value under
+bounds that reject mistakes, and with logits that are not finite (forms and bounds in
+mxfp4_router_reference)."""
 import numpy as np
 import pytest
 
@@ -29,6 +30,24 @@ def check_route_grad(mx, x, ids, dw, renormalize, counts, dloss):  # noqa: F811
     with np.errstate(all="ignore"):
         ref.check(got, want, bound + ref.rounded(np.abs(want) + bound, x.dtype), x.dtype)
     return got
+
+
+@pytest.mark.parametrize("dtype", FLOATS)
+@pytest.mark.parametrize("E", [7, 100, 200, 300, 600])
+@pytest.mark.parametrize("renormalize", [True, False])
+def test_lowest_values_as_masks(mx, dtype, E, renormalize):  # noqa: F811
+    say("router, lowest values %s E=%d %s" % (dtype, E, renormalize))
+    rng = np.random.default_rng(E)
+    info = torch.finfo(dtype)
+    x = gpu(rref.far_rows(rng, E, info.min, info.max)).to(dtype)
+    ids, _ = mx.route(x, 3)
+    dw = gpu(rng.standard_normal((12, 3)), torch.float32)
+    counts = check_balance(mx, x, ids)
+    assert int(counts[E]) == 12
+    one = torch.full((), 30.0, device="cuda")
+    check_route_grad(mx, x, ids, dw, renormalize, counts, one)
+    check_route_grad(mx, x, ids, dw, renormalize, None, None)
+    check_route_grad(mx, x, ids, None, renormalize, counts, one)
 
 
 @pytest.mark.parametrize("dtype", FLOATS)
