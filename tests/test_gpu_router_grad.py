@@ -1,6 +1,6 @@
-"""The balance loss and the router's gradient on the GPU with masks of the type's lowest value under
-bounds that reject mistakes, and with logits that are not finite (forms and bounds in
-mxfp4_router_reference)."""
+"""The balance loss and the router's gradient on the GPU over more tokens than the launches have
+lane groups, with masks of the type's lowest value under bounds that reject mistakes, and with
+logits that are not finite (forms and bounds in mxfp4_router_reference)."""
 import numpy as np
 import pytest
 
@@ -30,6 +30,45 @@ def check_route_grad(mx, x, ids, dw, renormalize, counts, dloss):  # noqa: F811
     with np.errstate(all="ignore"):
         ref.check(got, want, bound + ref.rounded(np.abs(want) + bound, x.dtype), x.dtype)
     return got
+
+
+def many(rng, T, E, k, dtype):
+    """Masked logits, every fifth row of -infinities, the k largest (ties to the lowest); in the
+    second half every seventh token names its first expert twice."""
+    x = gpu(rng.standard_normal((T, E)) * 2, torch.float32).to(dtype)
+    x[gpu(rng.random((T, E)) < 0.3)] = float("-inf")
+    x[3::5] = float("-inf")
+    top, ids = torch.sort(x.float(), dim=1, descending=True, stable=True)
+    ids = torch.where(top == float("-inf"), -1, ids)[:, :k].to(torch.int32).contiguous()
+    ids[T // 2::7, 1] = ids[T // 2::7, 0]
+    return x, ids
+
+
+# A launch of the gradient has 1024 blocks of 256 threads, of the loss 256 blocks of 512; a token
+# takes 8 lanes up to 64 experts, 16 up to 128, 32 up to 256, then 64: these walk three tokens or
+# more a lane group, the last round part-filled inside a wave.
+LONG = [(70001, 60, 4), (33001, 128, 8), (17003, 200, 3), (9001, 300, 5), (9001, 600, 3)]
+
+
+@pytest.mark.parametrize("dtype", FLOATS)
+@pytest.mark.parametrize("T,E,k", LONG)
+def test_several_tokens_a_lane_group(mx, dtype, T, E, k):  # noqa: F811
+    say("router, many tokens %s T=%d E=%d k=%d" % (dtype, T, E, k))
+    rng = np.random.default_rng([T, E, k])
+    x, ids = many(rng, T, E, k, dtype)
+    dw = gpu(rng.standard_normal((T, k)), torch.float32)
+    dloss = torch.full((), -3.5 * T, device="cuda")
+    counts = check_balance(mx, x, ids)
+    for renormalize in (True, False):
+        both = check_route_grad(mx, x, ids, dw, renormalize, counts, dloss)
+        check_route_grad(mx, x, ids, dw, renormalize, None, None)
+        assert (both[x == float("-inf")] == 0).all()
+        # a token's gradient does not depend on which lane group takes it, or when
+        for lo, hi in ((T - 1000, T), (T // 2 - 3, T // 2 + 500)):
+            part = mx.route_grad(x[lo:hi], ids[lo:hi], dw[lo:hi], renormalize=renormalize, counts=counts,
+                                 dloss=dloss)
+            assert torch.equal(part, both[lo:hi])
+    check_route_grad(mx, x, ids, None, True, counts, dloss)
 
 
 @pytest.mark.parametrize("dtype", FLOATS)
