@@ -231,7 +231,9 @@ int mxfp4_activation_grad(const void* dY, int dtype, int64_t R, int64_t y_stride
 
 /* Gradient through the weight-only product: dX[m,k] = sum_n dY[m,n] * W[n,k].
  *   dY in : fp16 or bf16 [M, N], rows y_stride elements apart (any N, element
- *           alignment; rows that start on 16 bytes are read fastest)
+ *           alignment; more than 16 rows are read fastest where N is a multiple of 8
+ *           and rows start on 16 bytes; 3001 of them take three to four times as long
+ *           elsewhere)
  *   W  in : MXFP4 codes [N, K/2] and scales [N, K/32]
  *   dX out: [M, K] of dY's dtype, dense, 16-byte aligned
  * Accuracy as mxfp4_linear, with N terms: |dX - exact| <= (N/8 + 64) 2^-24

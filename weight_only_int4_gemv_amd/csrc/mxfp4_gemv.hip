@@ -11,6 +11,7 @@
 // 12 weights in turn), of 14336 x 4096 10.5, of 28672 x 8192 29.5 (4.2 TB/s); the 16-row tiles of the
 // matrix cores, 64 bytes from each of 16 rows at a time, 16.5, 12.4 and 39.8.  Below 2^24 weights
 // (4096 x 4096 5.9 against 6.2 us, 1000 x 2048 4.5 against 3.7) the X in LDS costs more than it gains.
+// The weight-only INT4 row kernel reads as many bytes of 4096 x 14336 in 7.9 us.
 #include "mxfp4_act.h"
 
 namespace mxfp4 {
@@ -18,7 +19,9 @@ namespace {
 
 constexpr int kWaves = 8;
 constexpr int kRowsOfWave = 4;
-constexpr int kMaxX = 60000;                // bytes of X in LDS
+// Bytes of X in LDS: two blocks a CU hold twice as many, and no longer K was measured.  One row of
+// 3584 x 18944 takes 20.6 us on the 16-row tiles, of 8192 x 28672 45.7.
+constexpr int kMaxX = 60000;
 
 template <typename T>
 __global__ __launch_bounds__(kWaves* kWave, 4) void gemv_kernel(LinearArgs a, int split) {

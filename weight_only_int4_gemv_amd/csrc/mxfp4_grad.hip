@@ -671,7 +671,9 @@ typedef Tiling<2, 3, 3> Low;        // 32 x 256
 
 template <class C>
 void launch(GradArgs a, DType dt, hipStream_t stream) {
-    // The offset of a copy's rows has 32 bits.
+    // The offset of a copy's rows has 32 bits.  Where a row's last chunk is part-filled or rows do
+    // not start on 16 bytes, dY is read by element in every step: 3001 rows of 14336 x 4096 319 us,
+    // of 14335 x 4096 978, with rows 14335 apart 1353; of 50257 x 2048 2712, of 50256 624.
     const bool wide = (uintptr_t)a.dY % 16 == 0 && a.N % 8 == 0 &&
                       (a.R == 1 || (a.y_stride % 8 == 0 && a.y_stride <= 1 << 25));
     const int64_t nt = (a.K + kTiledCols - 1) / kTiledCols;

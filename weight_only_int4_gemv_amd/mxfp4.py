@@ -610,8 +610,9 @@ def linear_grad_workspace(M: int, N: int, K: int, device="cuda") -> torch.Tensor
 def linear_grad(dY: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
                 dX: torch.Tensor = None, workspace: torch.Tensor = None) -> torch.Tensor:
     """The gradient of linear() with respect to X: dY fp16 or bf16 [M, N] (dense rows)
-    times MXFP4 weights [N, K] -> dX [M, K] of dY's dtype, on 16 bytes.  Rows of dY that
-    start on 16 bytes are read fastest.  workspace: from linear_grad_workspace(), else
+    times MXFP4 weights [N, K] -> dX [M, K] of dY's dtype, on 16 bytes.  More than
+    16 rows are read fastest where N is a multiple of 8 and rows start on 16 bytes (3001 of
+    them take three to four times as long elsewhere).  workspace: from linear_grad_workspace(), else
     allocated per call where the shape uses one."""
     lib = library()
     N, K = _weights(codes, scales, 2)
